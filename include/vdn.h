@@ -397,6 +397,88 @@ VDN_API vdn_status vdn_hybrid_fuse_shard_rs(int L, int D, int H_local, int d, in
                                             void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Query/key preparation: rotary positions, alone or in one pass with the
+ * per-head norm of queries and keys.  vdn_vda_scan takes keys as given (unit
+ * length is the caller's); this is the pass that makes them, and the
+ * projections' gradients go back through it.
+ *
+ * Rotation plan.  The first rot_dim columns of every head form rot_dim / 2
+ * pairs: column i with i + rot_dim / 2 (VDN_ROPE_HALF) or 2i with 2i + 1
+ * (VDN_ROPE_INTERLEAVED).  Pair (a, b) of a row at position p becomes
+ *   (a cos - b sin, b cos + a sin) * scale,  at the angle p * frequency;
+ * the other columns pass through.  Positions are integers, on one to four
+ * axes (for example frame, row, column): the first section_pairs[0] pairs
+ * turn with axis 0, the next section_pairs[1] with axis 1, and so on.
+ *  - phase: device array [rot_dim / 2] of the pairs' frequencies in turns
+ *    per position (radians / 2 pi), modulo one turn, times 2^64.  Position
+ *    times phase modulo 2^64 is the angle with whole turns dropped, exact
+ *    for every 32-bit position, negative ones included.
+ *  - head_dim a multiple of 8 up to 256, rot_dim a multiple of 8 from 0 to
+ *    head_dim (VDN_ERR_UNSUPPORTED otherwise).
+ * ------------------------------------------------------------------------ */
+#define VDN_ROPE_HALF 0
+#define VDN_ROPE_INTERLEAVED 1
+
+/* element types of the calls that take a dtype */
+#define VDN_DTYPE_BF16 0
+#define VDN_DTYPE_F16 1
+#define VDN_DTYPE_F32 2
+
+/* n_i = x_i r w_i with r = 1 (NONE, no weight), (mean_i x_i^2 + eps)^-1/2
+ * (RMS) or (sum_i x_i^2 + eps)^-1/2 (L2), over the head's d columns */
+#define VDN_NORM_NONE 0
+#define VDN_NORM_RMS 1
+#define VDN_NORM_L2 2
+
+typedef struct {
+  int head_dim, rot_dim, layout, n_axes;
+  int section_pairs[4]; /* of the n_axes axes; they sum to rot_dim / 2 */
+  float scale;          /* factor of cos and sin (1 without one) */
+  const uint64_t* phase;
+} vdn_rope_plan;
+
+/* out = R(positions) x per row and head, or with `inverse` R^T, the gradient
+ * of the rotation (scale is applied in both).
+ * x, out   : [rows, ld] of dtype; out may be x itself (same ld), and may not
+ *            overlap it otherwise
+ * positions: device int32, axis a's at positions + a * pos_stride, one a
+ *            row; NULL: the row index on every axis
+ * rows may be 0 (nothing is enqueued).  No workspace. */
+VDN_API vdn_status vdn_rope(const vdn_rope_plan* plan, int dtype, int64_t rows, int H,
+                            const void* x, int64_t ld, const int32_t* positions,
+                            int64_t pos_stride, int inverse, void* out, int64_t ld_out,
+                            void* stream);
+
+/* q_out = R(p) norm(q), k_out = R(p) norm(k), per row and head, in one
+ * launch.  q has H heads and k H_kv; wq, wk: [head_dim] fp32 norm weights,
+ * shared by the heads, or NULL for ones.  Statistics and products in fp32,
+ * one rounding at the store.  q_out may be q and k_out k. */
+VDN_API vdn_status vdn_qk_norm_rope(const vdn_rope_plan* plan, int dtype, int64_t rows, int H,
+                                    int H_kv, const void* q, int64_t ld_q, const void* k,
+                                    int64_t ld_k, int q_norm, int k_norm, const float* wq,
+                                    const float* wk, float eps, const int32_t* positions,
+                                    int64_t pos_stride, void* q_out, int64_t ld_qo, void* k_out,
+                                    int64_t ld_ko, void* stream);
+
+/* Gradients of vdn_qk_norm_rope from its inputs and the gradients dq_out,
+ * dk_out of its outputs.  With g = R(p)^T dy:
+ *   dw_i = sum over rows and heads of g_i x_i r
+ *   dx_i = r w_i g_i - x_i r^3 c sum_j g_j w_j x_j,  c = 1/d (RMS), 1 (L2)
+ * dq, dk   : of dtype; dq may be dq_out and dk dk_out
+ * dwq, dwk : [head_dim] fp32, or NULL; sums in a fixed order (the same call
+ *            gives the same bits on the same GPU)
+ * ws       : >= vdn_qk_norm_rope_backward_workspace(head_dim) bytes */
+VDN_API size_t vdn_qk_norm_rope_backward_workspace(int head_dim);
+
+VDN_API vdn_status vdn_qk_norm_rope_backward(
+    const vdn_rope_plan* plan, int dtype, int64_t rows, int H, int H_kv, const void* q,
+    int64_t ld_q, const void* k, int64_t ld_k, int q_norm, int k_norm, const float* wq,
+    const float* wk, float eps, const int32_t* positions, int64_t pos_stride,
+    const void* dq_out, int64_t ld_dqo, const void* dk_out, int64_t ld_dko, void* dq,
+    int64_t ld_dq, void* dk, int64_t ld_dk, float* dwq, float* dwk, void* ws, size_t ws_bytes,
+    void* stream);
+
+/* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------ */
 

@@ -28,6 +28,8 @@ pages' description of the method:
                       beta and alpha (adjoint scans), for training the branch.
 * ``mxfp8``        -- MXFP8 quantization (E4M3 elements, UE8M0 block scales)
                       and the fuse with MXFP8 projections.
+* ``qk_prep``      -- per-head norm and rotary positions of queries and keys,
+                      and their gradients.
 
 The readings taken where the pages are silent are stated in each module's
 docstring.  Parity status of every function is pinned by the
@@ -40,7 +42,7 @@ from .window_attn import (frame_visible, visible_key_frames, window_attn,
                           window_attn_rows, mask_pair_count)
 from .fuse import sigmoid, rmsnorm_heads, fuse_gates, hybrid_fuse, hybrid_fuse_rows
 from .vda_backward import vda_backward
-from . import mxfp8
+from . import mxfp8, qk_prep
 
 __all__ = [
     "vda_prep", "vda_frame_state", "vda_scan", "vda_readout", "vda",
@@ -48,5 +50,5 @@ __all__ = [
     "frame_visible", "visible_key_frames", "window_attn", "window_attn_rows",
     "mask_pair_count",
     "sigmoid", "rmsnorm_heads", "fuse_gates", "hybrid_fuse", "hybrid_fuse_rows",
-    "vda_backward", "mxfp8",
+    "vda_backward", "mxfp8", "qk_prep",
 ]

@@ -8,6 +8,7 @@ device memory and the stream.  If the library is missing, every call raises
 
 import ctypes
 import functools
+import math
 import os
 
 import torch
@@ -32,7 +33,8 @@ EXPORTS = ["vdn_vda_scan_workspace", "vdn_vda_scan", "vdn_vda_debug_buffers",
            "vdn_hybrid_fuse_mxfp8_workspace", "vdn_hybrid_fuse_mxfp8",
            "vdn_hybrid_fuse_shard_rs", "vdn_window_attn_schedule",
            "vdn_window_attn_mxfp8_workspace", "vdn_window_attn_mxfp8", "vdn_copy2d_async",
-           "vdn_debug_bounds_enabled", "vdn_selftest_bounds"]
+           "vdn_debug_bounds_enabled", "vdn_selftest_bounds", "vdn_rope", "vdn_qk_norm_rope",
+           "vdn_qk_norm_rope_backward_workspace", "vdn_qk_norm_rope_backward"]
 
 SOLVER_CHOLESKY = 0
 SOLVER_GAUSS_JORDAN = 1
@@ -48,6 +50,12 @@ class VdnError(RuntimeError):
 class Shape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int),
                 ("d", ctypes.c_int)]
+
+
+class RopePlanC(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("n_axes", ctypes.c_int), ("section_pairs", ctypes.c_int * 4),
+                ("scale", ctypes.c_float), ("phase", ctypes.c_void_p)]
 
 
 _lib = None
@@ -144,6 +152,18 @@ def lib():
     L.vdn_window_attn_mxfp8.restype = ctypes.c_int
     L.vdn_copy2d_async.argtypes = [_P, _SZ, _P, _SZ, _SZ, _SZ, _P]
     L.vdn_copy2d_async.restype = ctypes.c_int
+    R = ctypes.POINTER(RopePlanC)
+    L.vdn_rope.argtypes = [R, ctypes.c_int, _I64, ctypes.c_int, _P, _I64, _P, _I64, ctypes.c_int,
+                           _P, _I64, _P]
+    L.vdn_rope.restype = ctypes.c_int
+    qk = [R, ctypes.c_int, _I64, ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, ctypes.c_int,
+          ctypes.c_int, _P, _P, ctypes.c_float, _P, _I64]
+    L.vdn_qk_norm_rope.argtypes = qk + [_P, _I64, _P, _I64, _P]
+    L.vdn_qk_norm_rope.restype = ctypes.c_int
+    L.vdn_qk_norm_rope_backward_workspace.argtypes = [ctypes.c_int]
+    L.vdn_qk_norm_rope_backward_workspace.restype = _SZ
+    L.vdn_qk_norm_rope_backward.argtypes = qk + [_P, _I64] * 4 + [_P, _P, _P, _SZ, _P]
+    L.vdn_qk_norm_rope_backward.restype = ctypes.c_int
     L.vdn_version.argtypes = []
     L.vdn_version.restype = ctypes.c_char_p
     _lib = L
@@ -568,6 +588,238 @@ def hybrid_fuse_shard_rs(x, o_s_local, o_vda_local, W_gs, W_gl, gamma, W_os, W_o
                                           len(owners), _ptr(ws), ws.numel(), _stream(stream))
     _check(code, "vdn_hybrid_fuse_shard_rs")
     return ws
+
+
+# ---------------------------------------------------------------- query/key preparation
+
+DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
+
+
+def _same_device(*ts):
+    """Every tensor on the current CUDA device (the kernels are launched there)."""
+    _need_cuda(*ts)
+    cur = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"libvdn: tensor on {t.device}, but the current device is cuda:{cur}")
+
+
+def _rows2d(name, t, cols, dtype, rows=None):
+    """t must be a [rows, >= cols] matrix with unit column stride and the dtype."""
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{rows or 'rows'}, {cols}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.shape[0] and t.shape[1] and t.stride(1) != 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+
+
+def _ld(t):
+    """Row stride in elements; one row or none has no stride of its own."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def rope_frequencies(rot, base=10000.0, sections=None, scaling=None, factor=1.0, original=4096,
+                     beta_fast=32.0, beta_slow=1.0):
+    """(radians per position of each pair, scale of cos and sin), in 64 bits.
+
+    Every axis a with n_a pairs (``sections``; one axis with all of rot / 2 by
+    default) has the series f_i = base^(-i / n_a).  ``scaling`` stretches it
+    for contexts ``factor`` times the trained length ``original``:
+      linear  f_i / factor (positions interpolated);
+      ntk     base * factor^(n_a / (n_a - 1)) in place of base: the fastest
+              pair is kept, the slowest is interpolated;
+      yarn    pairs that turn more than beta_fast times over ``original``
+              positions are kept, those below beta_slow turns interpolated, a
+              linear ramp in between, and cos and sin times
+              0.1 ln(factor) + 1 (Peng et al., arXiv 2309.00071).
+    """
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling: None, 'linear', 'ntk' or 'yarn'")
+    sections = [rot // 2] if sections is None else [int(n) for n in sections]
+    if any(n < 0 for n in sections) or sum(sections) != rot // 2:
+        raise ValueError("sections must sum to rot / 2")
+    if not (math.isfinite(base) and base > 1 and math.isfinite(factor) and factor > 0):
+        raise ValueError("base > 1 and factor > 0")
+    freq, scale = [], 1.0
+    for n in sections:
+        b = base * factor ** (n / (n - 1)) if scaling == "ntk" and n > 1 else base
+        f = [b ** (-i / n) for i in range(n)]
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "yarn":
+            def pair(turns):
+                return n * math.log(original / (turns * 2 * math.pi)) / math.log(base)
+            low = max(math.floor(pair(beta_fast)), 0)
+            high = min(math.ceil(pair(beta_slow)), 2 * n - 1)
+            ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(n)]
+            f = [x / factor * r + x * (1 - r) for x, r in zip(f, ramp)]
+        freq += f
+    if scaling == "yarn" and factor > 1:
+        scale = 0.1 * math.log(factor) + 1.0
+    return freq, scale
+
+
+class RopePlan:
+    """The rotation of rope() and qk_norm_rope(): pairs, axes and frequencies,
+    with the frequencies' fixed-point phases in device memory.
+
+    d: head dim; rot: rotated columns of each head (the first ones; default
+    all); layout: "half" or "interleaved"; sections: pairs of each position
+    axis (default: one axis).  The other arguments are rope_frequencies', or
+    ``frequencies`` gives the rot / 2 radians per position (and ``scale``)
+    directly.  Immutable; keep it for as long as calls that use it may run.
+    """
+
+    def __init__(self, d, rot=None, base=10000.0, layout="half", sections=None, scaling=None,
+                 factor=1.0, original=4096, beta_fast=32.0, beta_slow=1.0, frequencies=None,
+                 scale=None, device=None):
+        self.d = int(d)
+        self.rot = self.d if rot is None else int(rot)
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError("layout: 'half' or 'interleaved'")
+        if self.rot < 0 or self.rot > self.d or self.rot % 2:
+            raise ValueError("rot: an even number of the head's columns")
+        self.layout = layout
+        self.sections = [self.rot // 2] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(self.sections) <= 4:
+            raise ValueError("sections: one to four axes")
+        if frequencies is None:
+            self.frequencies, self.scale = rope_frequencies(
+                self.rot, base, self.sections, scaling, factor, original, beta_fast, beta_slow)
+        else:
+            self.frequencies, self.scale = [float(f) for f in frequencies], 1.0
+        if scale is not None:
+            self.scale = float(scale)
+        if len(self.frequencies) != self.rot // 2 or sum(self.sections) != self.rot // 2 or \
+                not all(math.isfinite(f) for f in self.frequencies):
+            raise ValueError("rot / 2 finite frequencies, and sections that sum to rot / 2")
+        words = [self.phase_word(f) for f in self.frequencies]
+        signed = [w - (1 << 64) if w >> 63 else w for w in words]
+        self.phase = torch.tensor(signed or [0], dtype=torch.int64).to(device or "cuda")
+
+    @staticmethod
+    def phase_word(radians):
+        """radians per position as turns x 2^64, modulo one turn."""
+        turns = math.fmod(radians / (2 * math.pi), 1.0)
+        return int(turns * 2.0 ** 64) & ((1 << 64) - 1)
+
+    @property
+    def n_axes(self):
+        return len(self.sections)
+
+    def _c(self):
+        pairs = (ctypes.c_int * 4)(*(self.sections + [0] * (4 - len(self.sections))))
+        return RopePlanC(self.d, self.rot, ROPE_LAYOUTS[self.layout], self.n_axes, pairs,
+                         self.scale, self.phase.data_ptr())
+
+
+def _rope_positions(positions, plan, rows):
+    """(pointer, axis stride) of int32 positions [rows] or [axes, rows]."""
+    if positions is None:
+        return None, 0
+    if positions.dtype != torch.int32:
+        raise ValueError("positions: int32")
+    p = positions[None] if positions.dim() == 1 else positions
+    if p.dim() != 2 or p.shape != (plan.n_axes, rows) or (rows > 1 and p.stride(1) != 1):
+        raise ValueError(f"positions: [{plan.n_axes}, {rows}] with contiguous rows")
+    return _ptr(p), p.stride(0) if plan.n_axes > 1 else rows
+
+
+def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
+    """Rotary positions on the H heads of x ([rows, H*d], bf16, fp16 or fp32):
+    out = R(positions) x, or with ``inverse`` R^T x, which is its gradient.
+    positions: int32 [rows] or [axes, rows], default the row index; out may
+    be x.  Returns out."""
+    _same_device(x, out, positions, plan.phase)
+    if x.dtype not in DTYPE_CODES:
+        raise ValueError("rope: bf16, fp16 or fp32")
+    _rows2d("x", x, H * plan.d, x.dtype)
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty((rows, H * plan.d), dtype=x.dtype, device=x.device)
+    _rows2d("out", out, H * plan.d, x.dtype, rows)
+    pos, stride = _rope_positions(positions, plan, rows)
+    c = plan._c()
+    _check(lib().vdn_rope(ctypes.byref(c), DTYPE_CODES[x.dtype], rows, int(H), _ptr(x), _ld(x),
+                          pos, stride, int(bool(inverse)), _ptr(out), _ld(out),
+                          _stream(stream)), "vdn_rope")
+    return out
+
+
+def _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions):
+    if q.dtype not in DTYPE_CODES:
+        raise ValueError("qk_norm_rope: bf16, fp16 or fp32")
+    if q_norm not in NORMS or k_norm not in NORMS:
+        raise ValueError("norm: 'rms', 'l2' or 'none'")
+    _rows2d("q", q, H * plan.d, q.dtype)
+    _rows2d("k", k, H_kv * plan.d, q.dtype, q.shape[0])
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (plan.d,) or
+                              not w.is_contiguous()):
+            raise ValueError(f"{name}: contiguous fp32 [{plan.d}]")
+    return _rope_positions(positions, plan, q.shape[0])
+
+
+def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rms", eps=1e-6,
+                 positions=None, q_out=None, k_out=None, stream=None):
+    """Per-head norm of q ([rows, H*d]) and k ([rows, H_kv*d]) and the rotation
+    in one pass.  Norms: "rms", "l2" (unit length, as vda_scan takes keys) or
+    "none"; wq, wk: fp32 [d] or None.  Outputs may be the inputs.
+    Returns (q_out, k_out)."""
+    _same_device(q, k, wq, wk, positions, q_out, k_out, plan.phase)
+    pos, stride = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions)
+    rows = q.shape[0]
+    if q_out is None:
+        q_out = torch.empty((rows, H * plan.d), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((rows, H_kv * plan.d), dtype=q.dtype, device=q.device)
+    _rows2d("q_out", q_out, H * plan.d, q.dtype, rows)
+    _rows2d("k_out", k_out, H_kv * plan.d, q.dtype, rows)
+    c = plan._c()
+    _check(lib().vdn_qk_norm_rope(
+        ctypes.byref(c), DTYPE_CODES[q.dtype], rows, int(H), int(H_kv), _ptr(q), _ld(q), _ptr(k),
+        _ld(k), NORMS[q_norm], NORMS[k_norm], _ptr(wq), _ptr(wk), float(eps), pos, stride,
+        _ptr(q_out), _ld(q_out), _ptr(k_out), _ld(k_out), _stream(stream)), "vdn_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None, q_norm="rms",
+                          k_norm="rms", eps=1e-6, positions=None, dq=None, dk=None, dwq=None,
+                          dwk=None, ws=None, stream=None):
+    """Gradients of qk_norm_rope from its inputs and its outputs' gradients.
+    Returns (dq, dk, dwq, dwk, ws): dwq and dwk fp32 [d], None where the side
+    has no norm.  dq may be dq_out and dk dk_out."""
+    _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
+    pos, stride = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions)
+    rows, dev = q.shape[0], q.device
+    if dq is None:
+        dq = torch.empty((rows, H * plan.d), dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty((rows, H_kv * plan.d), dtype=q.dtype, device=dev)
+    for name, t, h in (("dq_out", dq_out, H), ("dk_out", dk_out, H_kv), ("dq", dq, H),
+                       ("dk", dk, H_kv)):
+        _rows2d(name, t, h * plan.d, q.dtype, rows)
+    if dwq is None and NORMS[q_norm]:
+        dwq = torch.empty(plan.d, dtype=torch.float32, device=dev)
+    if dwk is None and NORMS[k_norm]:
+        dwk = torch.empty(plan.d, dtype=torch.float32, device=dev)
+    for name, w in (("dwq", dwq), ("dwk", dwk)):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (plan.d,) or
+                              not w.is_contiguous()):
+            raise ValueError(f"{name}: contiguous fp32 [{plan.d}]")
+    if ws is None:
+        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(plan.d)), dev)
+    c = plan._c()
+    _check(lib().vdn_qk_norm_rope_backward(
+        ctypes.byref(c), DTYPE_CODES[q.dtype], rows, int(H), int(H_kv), _ptr(q), _ld(q), _ptr(k),
+        _ld(k), NORMS[q_norm], NORMS[k_norm], _ptr(wq), _ptr(wk), float(eps), pos, stride,
+        _ptr(dq_out), _ld(dq_out), _ptr(dk_out), _ld(dk_out), _ptr(dq), _ld(dq), _ptr(dk),
+        _ld(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), ws.numel(), _stream(stream)),
+        "vdn_qk_norm_rope_backward")
+    return dq, dk, dwq, dwk, ws
 
 
 # ---------------------------------------------------------------- full layer
