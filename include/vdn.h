@@ -479,6 +479,51 @@ VDN_API vdn_status vdn_qk_norm_rope_backward(
     void* stream);
 
 /* ------------------------------------------------------------------------
+ * Attention with a sliding window and sinks, over packed sequences with
+ * shared key heads: the window Softmax of a causal stream (the first tokens
+ * stay visible, as the first-frame anchor does in vdn_window_attn), token by
+ * token.
+ *
+ * A sequence with n_q queries and n_k keys gives query i (from 0) the
+ * position p = i + n_k - n_q: the last query stands at the last key.  Query
+ * p sees key j iff
+ *     j <= p + ahead  and  (p - j < window  or  j < sinks)
+ * so window counts the query's own key, ahead = 0 is causal, and a window of
+ * at least n_k forgets nothing.
+ *     o_i = softmax over the visible keys of (scale q_i . k_j) v_j
+ * A query that sees nothing (an empty sequence of keys, or p + ahead < 0)
+ * gets o = 0 and lse = -inf.
+ *
+ * shape  : Lq, Lk rows in all; B sequences; H heads of q and o, H_kv of k and
+ *          v (H_kv divides H; head h reads key head h / (H / H_kv)); d 64 or
+ *          128 (VDN_ERR_UNSUPPORTED otherwise); window >= 1
+ * q, o   : [Lq, ld] bf16;  k, v: [Lk, ld_kv] bf16
+ * cu_q, cu_k: device int32 [B + 1], the first row of each sequence and the
+ *          end of the last, ascending; NULL for one sequence of all rows
+ *          (B = 1).  Rows that belong to no sequence are neither read into a
+ *          result nor written.  Values outside [0, L] are clamped.
+ * scale  : <= 0 selects 1/sqrt(d)
+ * lse_opt: NULL, or fp32 [H, Lq]: natural-log sum of exp(scaled scores)
+ * ws     : >= vdn_sink_attn_workspace(shape) bytes
+ * Products run in bf16 with fp32 accumulation, P rounded to bf16 for the
+ * product with V; sums and maxima in fp32.  A NaN or infinity in a key or
+ * value that some query of a 128-query tile sees can reach the other queries
+ * of that tile; rows of other sequences never do.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int Lq, Lk, B, H, H_kv, d;
+  int window, ahead, sinks;
+} vdn_sink_shape;
+
+VDN_API size_t vdn_sink_attn_workspace(const vdn_sink_shape* shape);
+
+VDN_API vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_q,
+                                 const void* k, const void* v, int64_t ld_kv,
+                                 const int32_t* cu_q, const int32_t* cu_k, float scale, void* o,
+                                 int64_t ld_o, float* lse_opt, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------ */
 

@@ -30,6 +30,8 @@ pages' description of the method:
                       and the fuse with MXFP8 projections.
 * ``qk_prep``      -- per-head norm and rotary positions of queries and keys,
                       and their gradients.
+* ``sink_attn``    -- attention with a sliding window and sinks, and its
+                      gradients.
 
 The readings taken where the pages are silent are stated in each module's
 docstring.  Parity status of every function is pinned by the
@@ -42,7 +44,7 @@ from .window_attn import (frame_visible, visible_key_frames, window_attn,
                           window_attn_rows, mask_pair_count)
 from .fuse import sigmoid, rmsnorm_heads, fuse_gates, hybrid_fuse, hybrid_fuse_rows
 from .vda_backward import vda_backward
-from . import mxfp8, qk_prep
+from . import mxfp8, qk_prep, sink_attn
 
 __all__ = [
     "vda_prep", "vda_frame_state", "vda_scan", "vda_readout", "vda",
@@ -50,5 +52,5 @@ __all__ = [
     "frame_visible", "visible_key_frames", "window_attn", "window_attn_rows",
     "mask_pair_count",
     "sigmoid", "rmsnorm_heads", "fuse_gates", "hybrid_fuse", "hybrid_fuse_rows",
-    "vda_backward", "mxfp8", "qk_prep",
+    "vda_backward", "mxfp8", "qk_prep", "sink_attn",
 ]

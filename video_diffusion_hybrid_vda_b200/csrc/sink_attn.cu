@@ -1,0 +1,629 @@
+// Attention with a sliding window and a few first tokens that stay visible
+// (sinks), over packed sequences with shared key heads: the forward pass.
+//
+//   s_ij = scale q_i . k_j over the visible keys (mask: sink_attn.cuh)
+//   o_i  = sum_j exp(s_ij - lse_i) v_j,   lse_i = log sum_j exp(s_ij)
+// A query that sees nothing gives o = 0 and lse = -inf.
+//
+// One pass over the keys with a running maximum and sum.  A CTA takes 256
+// queries (two 128-row tiles) of one sequence and head and walks the keys
+// they see between them in tiles of 128; a 128-row tile leaves out the key
+// tiles it does not touch (the window's two ends), and only key tiles that
+// cross the mask's edge pay for comparisons.
+//   warp 0      TMA: Q once, then K and V tiles through a two-stage ring; rows
+//               of a tile past its interval are zeroed before the tile is
+//               handed on
+//   warp 1      tcgen05.mma: S_i = Q_i K^T, O_i += P_i V (P_i from TMEM)
+//   warps 4-7   softmax of tile 0, warps 8-11 of tile 1, one query a thread
+// TMEM columns: S0 S1 O0 O1, 128 each; P_i overwrites S_i as bf16 (its
+// rounding averages out over the keys; the row sum adds the unrounded P).
+//
+// Few queries leave most SMs without a CTA: then the key tiles of each CTA are
+// split over several, each writes its normalised part in fp32 with its lse,
+// and sink_combine_kernel joins them, o = sum_s e^(lse_s - lse) o_s.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "exp2_fma.cuh"
+#include "sink_attn.cuh"
+
+namespace vdn {
+
+namespace {
+
+template <int DH>
+struct SinkCfg {
+  static constexpr int SLABS = DH / 64;
+  static constexpr int TILE_BYTES = SLABS * 128 * 128;  // 128 rows x DH bf16
+  static constexpr int STAGES = DH == 64 ? 4 : 2;
+  static constexpr int THREADS = 384;
+  static constexpr int SMEM = 1024 + 2 * TILE_BYTES + STAGES * 2 * TILE_BYTES + 512;
+};
+
+struct SinkOut {
+  __nv_bfloat16* o;  // [Lq, ld_o], or null where parts are written
+  int64_t ld_o;
+  float* lse;        // [H, Lq] or null
+  float* part_o;     // [splits, Lq, H, DH]
+  float* part_lse;   // [splits, H, Lq]
+};
+
+// Softmax of one 128-query tile: one thread per query.
+template <int DH>
+__device__ __forceinline__ void sink_softmax(int i, uint32_t tmem, uint64_t* s_full,
+                                             uint64_t* o_done, uint64_t* p_half,
+                                             uint64_t* p_ready, const SinkKeyTiles& kt, int j0,
+                                             int j1, const SinkMask& m, int pa, int pb,
+                                             float scale_log2, int row0, int row_end, int h,
+                                             const SinkDims& dims, const SinkOut& out, int split,
+                                             uint32_t* status, uint64_t budget_ns) {
+  const uint32_t quarter = warp_id() & 3;
+  const int row = quarter * 32 + lane_id();
+  const uint32_t lane_off = (quarter * 32) << 16;
+  const uint32_t s_addr = tmem + 128 * i + lane_off;
+  const uint32_t o_addr = tmem + 256 + 128 * i + lane_off;
+  const int p = pa + row;                // this query's position
+  const int pw = pa + quarter * 32;      // the warp's first
+  float m_used = -INFINITY;              // running maximum, log2 domain (scaled)
+  float l = 0.f;
+  int n = 0;                             // key tiles this query tile has taken
+  bool ok = true;
+  for (int j = j0; j < j1; ++j) {
+    const int ks = kt.start(j);
+    const int valid = kt.valid(j);
+    if (!sink_touches(m, pa, pb, ks, ks + valid - 1)) continue;
+    // warp-uniform decision: tcgen05.ld/st below are warp-collective
+    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[i], n & 1, budget_ns))) {
+      ok = false;
+      break;
+    }
+    tc_fence_after();
+    uint32_t sr[128];
+    uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+    uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+    uint32_t (&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
+    uint32_t (&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
+    const bool edge = valid < 128 || !sink_sees_all(m, pw, pw + 31, ks, ks + 127);
+    const int c_end = min(valid, p + m.ahead + 1 - ks);  // visible columns: below this, and
+    const int c_win = p - m.window + 1 - ks;             // from this on
+    const int c_sink = m.sinks - ks;                     // or below this
+    tmem_ld32(s_addr, s0);
+    tmem_ld32(s_addr + 32, s1);
+    tmem_ld_wait();
+    reg_fence(s0);
+    reg_fence(s1);
+    tmem_ld32(s_addr + 64, s2);
+    tmem_ld32(s_addr + 96, s3);
+    if (edge) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (c >= c_end || (c < c_win && c >= c_sink)) sr[c] = __float_as_uint(-INFINITY);
+    }
+    auto sv = [&](int c) { return __uint_as_float(sr[c]); };
+    float mx8[8];
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx8[a] = fmax3(sv(a), sv(a + 8), sv(a + 16));
+#pragma unroll
+    for (int c = 24; c < 56; c += 16)
+#pragma unroll
+      for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], sv(56 + a));
+    tmem_ld_wait();
+    reg_fence(s2);
+    reg_fence(s3);
+    if (edge) {
+#pragma unroll
+      for (int c = 64; c < 128; ++c)
+        if (c >= c_end || (c < c_win && c >= c_sink)) sr[c] = __float_as_uint(-INFINITY);
+    }
+#pragma unroll
+    for (int c = 64; c < 128; c += 16)
+#pragma unroll
+      for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
+    const float mt = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                           fmaxf(mx8[6], mx8[7])) *
+                     scale_log2;
+    // The maximum in use moves only when some row's grew by more than 2^8
+    // (then P stays below 2^8 and O is not rescaled for nothing).  A row that
+    // has seen no key keeps -inf: its factor is 0 and its P below takes 0.
+    if (__any_sync(0xffffffffu, mt > m_used + 8.f)) {
+      const float m_new = fmaxf(m_used, mt);
+      const float factor = m_used == -INFINITY ? 0.f : exp2_mufu(m_used - m_new);
+      l *= factor;
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c, o);
+          tmem_ld_wait();
+          reg_fence(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+          tmem_st32(o_addr + c, o);
+        }
+      }
+      m_used = m_new;
+    }
+    const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+    const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
+    const uint64_t nm = f32x2_pack(-m_sub, -m_sub);
+    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t xs = f32x2_fma(
+            (static_cast<uint64_t>(sr[32 * q + 2 * e + 1]) << 32) | sr[32 * q + 2 * e], cc, nm);
+        const uint64_t pp = f32x2_pack(exp2_mufu(f32x2_lo(xs)), exp2_mufu(f32x2_hi(xs)));
+        acc2[e & 3] = f32x2_add(acc2[e & 3], pp);
+        pk[e] = pack_bf16x2(f32x2_lo(pp), f32x2_hi(pp));
+      }
+      tmem_st16(s_addr + 16 * q, pk);
+      if (q == 1) {  // the product over the first 64 keys starts now
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_half[i]);
+      }
+    }
+    acc2[0] = f32x2_add(f32x2_add(acc2[0], acc2[1]), f32x2_add(acc2[2], acc2[3]));
+    l += f32x2_lo(acc2[0]) + f32x2_hi(acc2[0]);
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&p_ready[i]);
+    ++n;
+  }
+  // ------------------------------------------------------------ epilogue
+  ok = __all_sync(0xffffffffu, ok && (n == 0 || mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)));
+  if (!ok) {
+    record_status(status, kStatusTimeout);
+    return;
+  }
+  tc_fence_after();
+  const int r = row0 + row;
+  const bool live = r < row_end && in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH, DH,
+                                             static_cast<int64_t>(dims.H) * DH);
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: o = 0 (O holds no value if n == 0)
+  __nv_bfloat16* dst = out.o + static_cast<int64_t>(r) * out.ld_o + h * DH;
+  float* part = out.part_o + ((static_cast<int64_t>(split) * dims.Lq + r) * dims.H + h) * DH;
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    uint32_t o[32];
+    if (n > 0) {
+      tmem_ld32(o_addr + c, o);
+      tmem_ld_wait();
+      reg_fence(o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0;
+    }
+    if (!live) continue;
+    if (out.o != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint4 u;
+        u.x = pack_bf16x2(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
+        u.y = pack_bf16x2(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+        u.z = pack_bf16x2(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
+        u.w = pack_bf16x2(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
+        *reinterpret_cast<uint4*>(dst + c + e) = u;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4*>(part + c + e) =
+            make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+    }
+  }
+  if (!live) return;
+  const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+  const int64_t at = static_cast<int64_t>(h) * dims.Lq + r;
+  if (out.o == nullptr)
+    out.part_lse[static_cast<int64_t>(split) * dims.H * dims.Lq + at] = lse;
+  else if (out.lse != nullptr)
+    out.lse[at] = lse;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
+    sink_attn_kernel(const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const SinkDims dims, int splits,
+                     float scale_log2, const SinkOut out, uint32_t* status, uint64_t budget_ns) {
+  using Cfg = SinkCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* qbuf = smem;                         // Q0, Q1
+  uint8_t* kvbuf = smem + 2 * Cfg::TILE_BYTES;  // stage s: K then V
+  uint64_t* bars = reinterpret_cast<uint64_t*>(kvbuf + Cfg::STAGES * 2 * Cfg::TILE_BYTES);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;              // [STAGES]
+  uint64_t* v_full = k_full + Cfg::STAGES;  // [STAGES]
+  uint64_t* k_empty = v_full + Cfg::STAGES;
+  uint64_t* v_empty = k_empty + Cfg::STAGES;
+  uint64_t* s_full = v_empty + Cfg::STAGES;  // [2]
+  uint64_t* p_half = s_full + 2;             // [2] P of keys 0..63 stored
+  uint64_t* p_ready = p_half + 2;            // [2] all of P stored
+  uint64_t* o_done = p_ready + 2;            // [2]
+  uint64_t* mma_done = o_done + 2;
+  uint64_t* v_cut = mma_done + 1;            // V tiles whose last rows are zeroed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_cut + 1);
+
+  // Heaviest first: the last queries of a sequence see the most keys.
+  const int slots = sink_slots(dims.Lq, dims.B, 256);
+  const int per_slot = dims.H * splits;
+  const int slot = slots - 1 - static_cast<int>(blockIdx.x) / per_slot;
+  const int h = static_cast<int>(blockIdx.x) % per_slot / splits;
+  const int split = static_cast<int>(blockIdx.x) % splits;
+  const int hk = h / (dims.H / dims.Hkv);
+  const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 256, slot);
+  const SinkSeq seq = sink_seq(dims, b);
+  const int row0 = seq.q0 + 256 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 256));
+  if (row0 >= seq.q1) return;  // the whole CTA
+  // positions of the CTA's queries and of its two tiles (an empty tile 1 has
+  // pb < pa)
+  const int pa = row0 - seq.q0 + seq.shift();
+  const int pb = min(pa + 255, seq.nk() - 1);
+  const int pb0 = min(pa + 127, pb), pa1 = pa + 128;
+  SinkKeyTiles kt;
+  kt.init(dims.m, pa, pb, seq.nk());
+  const int j0 = static_cast<int>(static_cast<int64_t>(kt.n) * split / splits);
+  const int j1 = static_cast<int>(static_cast<int64_t>(kt.n) * (split + 1) / splits);
+  const uint32_t warp = warp_id();
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_half[i], 128);
+      mbar_init(&p_ready[i], 128);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(v_cut, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Register split (launched with 168 x 384 = 64512): 128 * 96 + 256 * 200 =
+  // 63488.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+  }
+  if (warp == 0) {
+    // ================================================================ TMA
+    // the whole warp walks the loop (it zeroes rows together); lane 0 issues
+    const bool leader = lane_id() == 0;
+    if (leader) {
+      mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
+      for (int i = 0; i < 2; ++i)
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(qbuf + i * Cfg::TILE_BYTES + sl * 16384, &qmap, q_full, h * DH + 64 * sl,
+                      row0 + 128 * i);
+    }
+    int issued_k = 0, issued_v = 0, cuts = 0;
+    bool ok = true;
+    for (int j = j0; j < j1 && ok; ++j) {
+      const int t = j - j0, s = t % Cfg::STAGES;
+      const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
+      uint8_t* kb = kvbuf + s * 2 * Cfg::TILE_BYTES;
+      uint8_t* vb = kb + Cfg::TILE_BYTES;
+      const int key0 = seq.k0 + kt.start(j);
+      const int valid = kt.valid(j);
+      if (t >= Cfg::STAGES)
+        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], par, budget_ns));
+      if (!ok) break;
+      if (leader) {
+        mbar_arrive_expect_tx(&k_full[s], Cfg::TILE_BYTES);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(kb + sl * 16384, &kmap, &k_full[s], hk * DH + 64 * sl, key0);
+      }
+      ++issued_k;
+      if (t >= Cfg::STAGES)
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], par, budget_ns));
+      if (!ok) break;
+      uint64_t* full = valid < 128 ? v_cut : &v_full[s];
+      if (leader) {
+        mbar_arrive_expect_tx(full, Cfg::TILE_BYTES);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(vb + sl * 16384, &vmap, full, hk * DH + 64 * sl, key0);
+      }
+      __syncwarp();
+      if (valid < 128) {
+        // the tile lands on a barrier of its own, loses its last rows, and
+        // is then handed on
+        ok = __all_sync(0xffffffffu, mbar_wait(v_cut, cuts & 1, budget_ns));
+        ++cuts;
+        if (!ok) break;
+        sink_zero_rows(vb, Cfg::SLABS, valid);
+        if (leader) mbar_arrive(&v_full[s]);
+      }
+      ++issued_v;
+    }
+    if (!ok) record_status(status, kStatusTimeout);
+    // no load may be in flight when the CTA ends
+    mbar_wait(q_full, 0, 200000000ull);
+    for (int t = max(0, issued_k - Cfg::STAGES); t < issued_k; ++t)
+      mbar_wait(&k_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
+    for (int t = max(0, issued_v - Cfg::STAGES); t < issued_v; ++t)
+      mbar_wait(&v_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
+    if (cuts > 0) mbar_wait(v_cut, (cuts - 1) & 1, 200000000ull);
+  } else if (warp == 1) {
+    // ================================================================ MMA
+    if (elect_one()) {
+      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16(128, DH, false, true);
+      const uint32_t qb = smem_u32(qbuf);
+      bool ok = mbar_wait(q_full, 0, budget_ns);
+      int done[2] = {0, 0};  // key tiles each query tile has taken
+      auto takes = [&](int i, int j) {
+        const int ks = kt.start(j);
+        return sink_touches(dims.m, i ? pa1 : pa, i ? pb : pb0, ks, ks + kt.valid(j) - 1);
+      };
+      auto issue_s = [&](int i, int j) {
+        if (!takes(i, j)) return;
+        const uint32_t kb = smem_u32(kvbuf + (j - j0) % Cfg::STAGES * 2 * Cfg::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_ss(tmem + 128 * i, sdesc_sw128(qb + i * Cfg::TILE_BYTES + off, 16, 1024),
+                  sdesc_sw128(kb + off, 16, 1024), idesc_s, kk > 0);
+        }
+        umma_commit(&s_full[i]);
+      };
+      // O_i += P_i V of tile j, the first 64 keys as soon as their P is there
+      auto issue_o = [&](int i, int j) {
+        if (!takes(i, j)) return true;
+        const uint32_t vb = smem_u32(kvbuf + (j - j0) % Cfg::STAGES * 2 * Cfg::TILE_BYTES +
+                                     Cfg::TILE_BYTES);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(half ? &p_ready[i] : &p_half[i], done[i] & 1, budget_ns)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            umma_ts(tmem + 256 + 128 * i, tmem + 128 * i + kk * 8,
+                    sdesc_sw128(vb + kk * 2048, 16384, 1024), idesc_o, done[i] > 0 || kk > 0);
+        }
+        umma_commit(&o_done[i]);
+        ++done[i];
+        return true;
+      };
+      if (ok && j0 < j1 && (ok = mbar_wait(&k_full[0], 0, budget_ns))) {
+        tc_fence_after();
+        issue_s(0, j0);
+        issue_s(1, j0);
+        umma_commit(&k_empty[0]);
+      }
+      for (int j = j0; j < j1 && ok; ++j) {
+        const int t = j - j0, s = t % Cfg::STAGES, sn = (t + 1) % Cfg::STAGES;
+        const bool more = j + 1 < j1;
+        if (!(ok = mbar_wait(&v_full[s], (t / Cfg::STAGES) & 1, budget_ns))) break;
+        tc_fence_after();
+        if (!(ok = issue_o(0, j))) break;
+        if (more) {
+          if (!(ok = mbar_wait(&k_full[sn], ((t + 1) / Cfg::STAGES) & 1, budget_ns))) break;
+          tc_fence_after();
+          issue_s(0, j + 1);
+        }
+        if (!(ok = issue_o(1, j))) break;
+        umma_commit(&v_empty[s]);
+        if (more) {
+          issue_s(1, j + 1);
+          umma_commit(&k_empty[sn]);
+        }
+      }
+      if (!ok) record_status(status, kStatusTimeout);
+      umma_commit(mma_done);
+    }
+  } else if (warp >= 4) {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    const int i = (warp - 4) >> 2;
+    sink_softmax<DH>(i, tmem, s_full, o_done, p_half, p_ready, kt, j0, j1, dims.m,
+                     i ? pa1 : pa, i ? pb : pb0, scale_log2, row0 + 128 * i, seq.q1, h, dims, out,
+                     split, status, budget_ns);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    mbar_wait(mma_done, 0, 200000000ull);
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// o and lse of (row, head) from its parts: a warp each, DH / 32 columns a lane.
+template <int DH>
+__global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, int splits,
+                                                           const SinkOut parts,
+                                                           __nv_bfloat16* __restrict__ o,
+                                                           int64_t ld_o,
+                                                           float* __restrict__ lse) {
+  constexpr int W = DH / 32;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
+  const int r = static_cast<int>(w / dims.H), h = static_cast<int>(w % dims.H);
+  if (r >= dims.Lq) return;
+  if (dims.cu_q != nullptr &&  // rows of no sequence have no parts and stay as they are
+      (r < sink_bound(dims.cu_q, 0, dims.Lq) || r >= sink_bound(dims.cu_q, dims.B, dims.Lq)))
+    return;
+  const int64_t at = static_cast<int64_t>(h) * dims.Lq + r, step = static_cast<int64_t>(dims.H) *
+                                                                   dims.Lq;
+  float top = -INFINITY;
+  for (int s = 0; s < splits; ++s) top = fmaxf(top, parts.part_lse[s * step + at]);
+  float sum = 0.f, acc[W] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float part = parts.part_lse[s * step + at];
+    if (part == -INFINITY) continue;  // saw nothing (a NaN goes through)
+    const float f = __expf(part - top);
+    sum += f;
+    const float* src = parts.part_o + ((static_cast<int64_t>(s) * dims.Lq + r) * dims.H + h) * DH;
+#pragma unroll
+    for (int c = 0; c < W; ++c) acc[c] += f * src[32 * c + lane_id()];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int c = 0; c < W; ++c)
+    o[static_cast<int64_t>(r) * ld_o + h * DH + 32 * c + lane_id()] = __float2bfloat16(acc[c] *
+                                                                                       inv);
+  if (lse != nullptr && lane_id() == 0) lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+// Splits of each CTA's key tiles: only where the CTAs would leave most of 148
+// SMs idle, with four key tiles (512 keys) at least a split.  Depends on the
+// shape alone, since the workspace does.
+int sink_splits(const vdn_sink_shape& s) {
+  const int64_t ctas = static_cast<int64_t>(sink_slots(s.Lq, s.B, 256)) * s.H;
+  if (ctas > 74) return 1;
+  int64_t keys = static_cast<int64_t>(s.window) + s.ahead + 256 + s.sinks;
+  if (keys > s.Lk) keys = s.Lk;
+  const int64_t most = (keys + 127) / 128 / 4;
+  int64_t n = 148 / ctas;
+  n = n > most ? most : n;
+  n = n > 32 ? 32 : n;
+  return n < 1 ? 1 : static_cast<int>(n);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int DH>
+cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, int splits,
+                        const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                        float scale, __nv_bfloat16* o, int64_t ld_o, float* lse, uint8_t* ws) {
+  using Cfg = SinkCfg<DH>;
+  static std::atomic<uint64_t> smem_set{0};
+  if (cudaError_t e = set_smem_once(sink_attn_kernel<DH>, Cfg::SMEM, smem_set)) return e;
+  SinkOut out{};
+  out.o = splits == 1 ? o : nullptr;
+  out.ld_o = ld_o;
+  out.lse = lse;
+  out.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
+  out.part_lse = reinterpret_cast<float*>(
+      ws + kStatusBytes +
+      align256(static_cast<size_t>(splits) * dims.Lq * dims.H * DH * sizeof(float)));
+  const int grid = sink_slots(dims.Lq, dims.B, 256) * dims.H * splits;
+  sink_attn_kernel<DH><<<grid, Cfg::THREADS, Cfg::SMEM, ctx.stream>>>(
+      qmap, kmap, vmap, dims, splits, scale * 1.4426950408889634f, out, ctx.status,
+      ctx.budget_ns);
+  if (cudaError_t e = cudaGetLastError()) return e;
+  if (splits > 1) {
+    const int64_t warps = static_cast<int64_t>(dims.Lq) * dims.H;
+    sink_combine_kernel<DH><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, ctx.stream>>>(
+        dims, splits, out, o, ld_o, lse);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Checks shared by the forward and the gradient call; `s` gets the clamped
+// mask.
+vdn_status sink_check(const vdn_sink_shape* shape, const void* q, int64_t ld_q, const void* k,
+                      const void* v, int64_t ld_kv, const int32_t* cu_q, const int32_t* cu_k,
+                      vdn_sink_shape* s) {
+  if (shape == nullptr) return VDN_ERR_INVALID_ARG;
+  *s = *shape;
+  if (s->Lq < 0 || s->Lk < 0 || s->Lq > kSinkMax - 1024 || s->Lk > kSinkMax - 1024 || s->B < 1 ||
+      s->B > (1 << 20) || s->H < 1 || s->H_kv < 1 || s->H % s->H_kv || s->d < 1)
+    return VDN_ERR_INVALID_ARG;
+  if (s->d != 64 && s->d != 128) return VDN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(s->H) * s->d >= (int64_t(1) << 24)) return VDN_ERR_INVALID_ARG;
+  if (s->window < 1 || s->ahead < 0 || s->sinks < 0) return VDN_ERR_INVALID_ARG;
+  if (s->window > kSinkMax) s->window = kSinkMax;
+  if (s->ahead > kSinkMax) s->ahead = kSinkMax;
+  if (s->sinks > kSinkMax) s->sinks = kSinkMax;
+  auto bad = [](const void* p, int rows) {
+    return (p == nullptr && rows > 0) || (reinterpret_cast<uintptr_t>(p) & 15u);
+  };
+  if (bad(q, s->Lq) || bad(k, s->Lk) || bad(v, s->Lk)) return VDN_ERR_INVALID_ARG;
+  if (ld_q < static_cast<int64_t>(s->H) * s->d || ld_q % 8 ||
+      ld_kv < static_cast<int64_t>(s->H_kv) * s->d || ld_kv % 8)
+    return VDN_ERR_INVALID_ARG;
+  if (s->B > 1 && (cu_q == nullptr || cu_k == nullptr)) return VDN_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(cu_q) & 3u) || (reinterpret_cast<uintptr_t>(cu_k) & 3u))
+    return VDN_ERR_INVALID_ARG;
+  return VDN_OK;
+}
+
+}  // namespace vdn
+
+using namespace vdn;
+
+extern "C" {
+
+size_t vdn_sink_attn_workspace(const vdn_sink_shape* shape) {
+  vdn_sink_shape s;
+  const void* p = reinterpret_cast<const void*>(256);
+  if (shape == nullptr ||
+      sink_check(shape, p, (int64_t)1 << 24, p, p, (int64_t)1 << 24,
+                 static_cast<const int32_t*>(p), static_cast<const int32_t*>(p), &s) != VDN_OK)
+    return 0;
+  const int n = sink_splits(s);
+  if (n == 1) return kStatusBytes;
+  const size_t rows = static_cast<size_t>(n) * s.Lq * s.H;
+  return kStatusBytes + align256(rows * s.d * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_q, const void* k,
+                         const void* v, int64_t ld_kv, const int32_t* cu_q, const int32_t* cu_k,
+                         float scale, void* o, int64_t ld_o, float* lse_opt, void* ws,
+                         size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("vdn_sink_attn");
+  vdn_sink_shape s;
+  const vdn_status r = sink_check(shape, q, ld_q, k, v, ld_kv, cu_q, cu_k, &s);
+  if (r != VDN_OK) return r;
+  const int64_t D = static_cast<int64_t>(s.H) * s.d, Dk = static_cast<int64_t>(s.H_kv) * s.d;
+  if ((o == nullptr && s.Lq > 0) || (reinterpret_cast<uintptr_t>(o) & 15u) || ld_o < D ||
+      ld_o % 8 || (reinterpret_cast<uintptr_t>(lse_opt) & 3u))
+    return VDN_ERR_INVALID_ARG;
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) ||
+      ws_bytes < vdn_sink_attn_workspace(shape))
+    return VDN_ERR_WORKSPACE;
+  if (s.Lq == 0) return VDN_OK;
+  const int splits = sink_splits(s);
+  if (static_cast<int64_t>(sink_slots(s.Lq, s.B, 256)) * s.H * splits >= (int64_t(1) << 31) ||
+      static_cast<int64_t>(s.Lq) * s.H >= (int64_t(1) << 33))
+    return VDN_ERR_UNSUPPORTED;
+  const SinkDims dims{s.Lq, s.Lk, s.B, s.H, s.H_kv, cu_q, cu_k, {s.window, s.ahead, s.sinks}};
+  CUtensorMap qmap, kmap, vmap;
+  if (!make_rows_map(&qmap, q, D, ld_q, s.Lq, 128)) return VDN_ERR_CUDA;
+  kmap = vmap = qmap;  // no keys: never loaded
+  if (s.Lk > 0 && (!make_rows_map(&kmap, k, Dk, ld_kv, s.Lk, 128) ||
+                   !make_rows_map(&vmap, v, Dk, ld_kv, s.Lk, 128)))
+    return VDN_ERR_CUDA;
+  const Launch ctx{static_cast<cudaStream_t>(stream), static_cast<uint32_t*>(ws),
+                   current_wait_budget_ns()};
+  const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
+  auto* ob = static_cast<__nv_bfloat16*>(o);
+  auto* wb = static_cast<uint8_t*>(ws);
+  const cudaError_t e =
+      s.d == 128 ? launch_sink<128>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, wb)
+                 : launch_sink<64>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, wb);
+  return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -34,7 +34,8 @@ EXPORTS = ["vdn_vda_scan_workspace", "vdn_vda_scan", "vdn_vda_debug_buffers",
            "vdn_hybrid_fuse_shard_rs", "vdn_window_attn_schedule",
            "vdn_window_attn_mxfp8_workspace", "vdn_window_attn_mxfp8", "vdn_copy2d_async",
            "vdn_debug_bounds_enabled", "vdn_selftest_bounds", "vdn_rope", "vdn_qk_norm_rope",
-           "vdn_qk_norm_rope_backward_workspace", "vdn_qk_norm_rope_backward"]
+           "vdn_qk_norm_rope_backward_workspace", "vdn_qk_norm_rope_backward",
+           "vdn_sink_attn_workspace", "vdn_sink_attn"]
 
 SOLVER_CHOLESKY = 0
 SOLVER_GAUSS_JORDAN = 1
@@ -56,6 +57,11 @@ class RopePlanC(ctypes.Structure):
     _fields_ = [("head_dim", ctypes.c_int), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
                 ("n_axes", ctypes.c_int), ("section_pairs", ctypes.c_int * 4),
                 ("scale", ctypes.c_float), ("phase", ctypes.c_void_p)]
+
+
+class SinkShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("Lq", "Lk", "B", "H", "H_kv", "d", "window", "ahead",
+                                            "sinks")]
 
 
 _lib = None
@@ -164,6 +170,12 @@ def lib():
     L.vdn_qk_norm_rope_backward_workspace.restype = _SZ
     L.vdn_qk_norm_rope_backward.argtypes = qk + [_P, _I64] * 4 + [_P, _P, _P, _SZ, _P]
     L.vdn_qk_norm_rope_backward.restype = ctypes.c_int
+    K = ctypes.POINTER(SinkShape)
+    L.vdn_sink_attn_workspace.argtypes = [K]
+    L.vdn_sink_attn_workspace.restype = _SZ
+    L.vdn_sink_attn.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P, _I64, _P,
+                                _P, _SZ, _P]
+    L.vdn_sink_attn.restype = ctypes.c_int
     L.vdn_version.argtypes = []
     L.vdn_version.restype = ctypes.c_char_p
     _lib = L
@@ -820,6 +832,65 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
         _ld(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), ws.numel(), _stream(stream)),
         "vdn_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
+
+
+# ---------------------------------------------------------------- sink-window attention
+
+_INT_MAX = (1 << 31) - 1
+
+
+def _sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead):
+    window = _INT_MAX if window is None else min(int(window), _INT_MAX)
+    return SinkShape(int(Lq), int(Lk), int(B), int(H), int(H_kv), int(d), window,
+                     min(int(ahead), _INT_MAX), min(int(sinks), _INT_MAX))
+
+
+def sink_attn_workspace(Lq, Lk, B, H, H_kv, d, window, sinks=0, ahead=0):
+    return int(lib().vdn_sink_attn_workspace(
+        ctypes.byref(_sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead))))
+
+
+def _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k):
+    _rows2d("q", q, H * d, torch.bfloat16)
+    _rows2d("k", k, H_kv * d, torch.bfloat16)
+    _rows2d("v", v, H_kv * d, torch.bfloat16, k.shape[0])
+    if _ld(k) != _ld(v):
+        raise ValueError("k and v must share one row stride")
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k: both or neither")
+    B = 1
+    if cu_q is not None:
+        if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32 or cu_q.dim() != 1 or \
+                cu_q.shape != cu_k.shape or cu_q.numel() < 2 or not cu_q.is_contiguous() or \
+                not cu_k.is_contiguous():
+            raise ValueError("cu_q and cu_k: contiguous int32 [sequences + 1]")
+        B = cu_q.numel() - 1
+    return _sink_shape(q.shape[0], k.shape[0], B, H, H_kv, d, window, sinks, ahead)
+
+
+def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=None, scale=0.0,
+              out=None, lse=None, ws=None, stream=None):
+    """Attention with a sliding window and sinks over packed sequences.
+
+    q [Lq, H*d], k and v [Lk, H_kv*d] bf16.  Query at position p sees key j
+    iff j <= p + ahead and (p - j < window or j < sinks); the last query of a
+    sequence stands at its last key.  window None forgets nothing.  cu_q,
+    cu_k: int32 [B + 1] row offsets of the sequences (None: one sequence).
+    Returns (o, ws); fills ``lse`` [H, Lq] if given."""
+    _same_device(q, k, v, cu_q, cu_k, out, lse, ws)
+    shape = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k)
+    if out is None:
+        out = torch.empty((q.shape[0], H * d), dtype=torch.bfloat16, device=q.device)
+    _rows2d("out", out, H * d, torch.bfloat16, q.shape[0])
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, q.shape[0]) or
+                            not lse.is_contiguous()):
+        raise ValueError("lse: contiguous fp32 [H, Lq]")
+    if ws is None:
+        ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(ctypes.byref(shape))), q.device)
+    _check(lib().vdn_sink_attn(ctypes.byref(shape), _ptr(q), _ld(q), _ptr(k), _ptr(v), _ld(k),
+                               _ptr(cu_q), _ptr(cu_k), float(scale), _ptr(out), _ld(out),
+                               _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "vdn_sink_attn")
+    return out, ws
 
 
 # ---------------------------------------------------------------- full layer
