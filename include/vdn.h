@@ -523,6 +523,25 @@ VDN_API vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int
                                  int64_t ld_o, float* lse_opt, void* ws, size_t ws_bytes,
                                  void* stream);
 
+/* Gradients of vdn_sink_attn from its inputs, its o and lse, and d_o =
+ * dLoss/do.  Deterministic: the same call gives the same bits.
+ * o, d_o   : [Lq, ld] bf16;  lse: fp32 [H, Lq] (of the forward call)
+ * dq       : [Lq, ld_dq] bf16;  dk, dv: [Lk, ld_dkv] bf16; none may overlap
+ *            an input.  Rows of no sequence are not written; keys that no
+ *            query sees and queries that see nothing get zeros.
+ * ws       : >= vdn_sink_attn_backward_workspace(shape) bytes
+ * P and dS are rounded to bf16 for their products; sums in fp32. */
+VDN_API size_t vdn_sink_attn_backward_workspace(const vdn_sink_shape* shape);
+
+VDN_API vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q,
+                                          int64_t ld_q, const void* k, const void* v,
+                                          int64_t ld_kv, const int32_t* cu_q,
+                                          const int32_t* cu_k, float scale, const void* o,
+                                          int64_t ld_o, const float* lse, const void* d_o,
+                                          int64_t ld_do, void* dq, int64_t ld_dq, void* dk,
+                                          void* dv, int64_t ld_dkv, void* ws, size_t ws_bytes,
+                                          void* stream);
+
 /* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------ */

@@ -134,3 +134,28 @@ def test_workspaces(L):
     none = _shape(L, Lq=0)
     assert lib.vdn_sink_attn(ctypes.byref(none), None, 512, P(A), P(A), 256, None, None, 0.0,
                              None, 512, None, P(A), 256, None) == 0
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q=0), 1), (dict(o=0), 1), (dict(lse=0), 1), (dict(d_o=A + 8), 1), (dict(dq=0), 1),
+    (dict(dk=A + 4), 1), (dict(dv=0), 1), (dict(ld_dq=500), 1), (dict(ld_dkv=128), 1),
+    (dict(lse=A + 1), 1), (dict(ws=0), 3), (dict(ws=A + 16), 3), (dict(ws_bytes=256), 3)])
+def test_bad_gradient_arguments_are_refused_on_the_host(L, change, code):
+    lib, P = L.lib(), ctypes.c_void_p
+    a = dict(q=A, o=A, lse=A, d_o=A, dq=A, dk=A, dv=A, ld_dq=512, ld_dkv=256, ws=A,
+             ws_bytes=1 << 40)
+    a.update(change)
+    s = _shape(L)
+    assert lib.vdn_sink_attn_backward(
+        ctypes.byref(s), P(a["q"]), 512, P(A), P(A), 256, None, None, 0.0, P(a["o"]), 512,
+        P(a["lse"]), P(a["d_o"]), 512, P(a["dq"]), a["ld_dq"], P(a["dk"]), P(a["dv"]),
+        a["ld_dkv"], P(a["ws"]), a["ws_bytes"], None) == code
+
+
+@pytest.mark.parametrize("change,code", BAD_SHAPES)
+def test_bad_gradient_shapes_are_refused_on_the_host(L, change, code):
+    lib, P = L.lib(), ctypes.c_void_p
+    s = _shape(L, **change)
+    assert lib.vdn_sink_attn_backward(
+        ctypes.byref(s), P(A), 512, P(A), P(A), 256, None, None, 0.0, P(A), 512, P(A), P(A), 512,
+        P(A), 512, P(A), P(A), 256, P(A), 1 << 40, None) == code

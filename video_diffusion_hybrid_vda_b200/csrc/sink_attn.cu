@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
         // the tile lands on a barrier of its own, loses its last rows, and
         // is then handed on
         ok = __all_sync(0xffffffffu, mbar_wait(v_cut, cuts & 1, budget_ns));
-        ++cuts;
         if (!ok) break;
+        ++cuts;
         sink_zero_rows(vb, Cfg::SLABS, valid);
         if (leader) mbar_arrive(&v_full[s]);
       }
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
       mbar_wait(&k_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
     for (int t = max(0, issued_v - Cfg::STAGES); t < issued_v; ++t)
       mbar_wait(&v_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
-    if (cuts > 0) mbar_wait(v_cut, (cuts - 1) & 1, 200000000ull);
+    if (!ok) mbar_wait(v_cut, cuts & 1, 200000000ull);  // a cut tile's load may be in flight
   } else if (warp == 1) {
     // ================================================================ MMA
     if (elect_one()) {

@@ -1,0 +1,997 @@
+// Gradients of attention with a sliding window and sinks (sink_attn.cu).
+//
+// With P_ij = exp(scale q_i . k_j - lse_i) over the visible keys and
+// D_i = dO_i . o_i:
+//   dV_j = sum_i P_ij dO_i
+//   dS_ij = P_ij (dO_i . v_j - D_i)
+//   dQ_i = scale sum_j dS_ij k_j,   dK_j = scale sum_i dS_ij q_i
+// A query that saw nothing (lse = -inf) contributes nothing and gets dQ = 0.
+//
+// P is formed anew from q, k and lse.  Two passes, so that every sum has one
+// owner and a fixed order (the same call gives the same bits): the key pass
+// holds dK and dV of 128 keys of one key head and walks the queries of all its
+// query heads; the query pass holds dQ of 128 queries.  That is seven products
+// a pair of tiles where one pass with atomic adds into dQ would take five.
+// P and dS are rounded to bf16 for their products, sums stay fp32 in TMEM.
+//
+// A sink key is seen by every later query, a key behind it by `window` of
+// them.  Where that leaves the few tiles with sinks far longer than the rest,
+// the queries past the window's reach are split over further CTAs whose fp32
+// sums the owner of the tile adds in order ("far" parts).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "exp2_fma.cuh"
+#include "sink_attn.cuh"
+
+namespace vdn {
+
+vdn_status sink_check(const vdn_sink_shape* shape, const void* q, int64_t ld_q, const void* k,
+                      const void* v, int64_t ld_kv, const int32_t* cu_q, const int32_t* cu_k,
+                      vdn_sink_shape* s);
+
+namespace {
+
+constexpr int kThreads = 384;
+
+template <int DH>
+struct GradCfg {
+  static constexpr int SLABS = DH / 64;
+  static constexpr int TILE = SLABS * 128 * 128;  // 128 rows x DH bf16
+  static constexpr int STAGES = 2;
+  static constexpr int STATS = 2 * 128 * 4;       // -lse log2 e and D of 128 queries
+  // two resident tiles, a ring of two-tile stages, statistics, barriers
+  static constexpr int SMEM = 1024 + 2 * TILE + STAGES * (2 * TILE + STATS) + 512;
+};
+
+// Per query, in tiles of 128 (the slots of sink_attn.cuh): -lse log2 e and
+// D = dO . o.  Rows past the sequence's end get -inf and 0: P = 0 there.
+__global__ void __launch_bounds__(256) sink_stats_kernel(
+    const SinkDims dims, int DH, const __nv_bfloat16* __restrict__ o, int64_t ld_o,
+    const __nv_bfloat16* __restrict__ d_o, int64_t ld_do, const float* __restrict__ lse,
+    float* __restrict__ nlse2, float* __restrict__ delta) {
+  // a block: 32 rows of a slot, all heads; DH / 8 lanes a (row, head)
+  const int slot = blockIdx.x >> 2;
+  const int slots = sink_slots(dims.Lq, dims.B, 128);
+  const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
+  const SinkSeq seq = sink_seq(dims, b);
+  const int tile0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
+  if (tile0 >= seq.q1) return;
+  const int first = (blockIdx.x & 3) * 32;
+  const int lanes = DH / 8, step = 256 / lanes;
+  const int lane = threadIdx.x % lanes;
+  // rows innermost in the slot order of a warp's lanes would scatter the
+  // loads; heads innermost read whole rows
+  for (int base = 0; base < 32 * dims.H; base += step) {
+    const int s = base + threadIdx.x / lanes;
+    const int i = s / dims.H, h = s - i * dims.H;
+    const int r = tile0 + first + i;
+    float t = 0.f;
+    const bool on = i < 32 && r < seq.q1;
+    if (on) {
+      const uint4 x = *reinterpret_cast<const uint4*>(o + r * ld_o + h * DH + 8 * lane);
+      const uint4 y = *reinterpret_cast<const uint4*>(d_o + r * ld_do + h * DH + 8 * lane);
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = unpack_bf16x2(xs[e]), c = unpack_bf16x2(ys[e]);
+        t += a.x * c.x + a.y * c.y;
+      }
+    }
+    for (int w = lanes >> 1; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+    if (lane == 0 && i < 32) {
+      const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + first + i;
+      const float v = on ? lse[static_cast<int64_t>(h) * dims.Lq + r] : -INFINITY;
+      const bool none = v == -INFINITY;
+      nlse2[at] = none ? -INFINITY : -v * 1.4426950408889634f;
+      delta[at] = none ? 0.f : t;
+    }
+  }
+}
+
+// A operand (128 x 128 bf16 in TMEM, packed by the two warpgroups into words
+// [0, 32) and [64, 96) of its 128 columns) times 128 rows of `b_tile`
+// (MN-major), the half of the 128 that warpgroup w wrote.
+template <int DH>
+__device__ __forceinline__ void grad_mma_half(uint32_t d, uint32_t a, uint32_t b_tile, int w,
+                                              bool accumulate) {
+  constexpr uint32_t idesc = idesc_bf16(128, DH, false, true);
+#pragma unroll
+  for (int kk = 0; kk < 4; ++kk)
+    umma_ts(d, a + 64 * w + 8 * kk, sdesc_sw128(b_tile + (4 * w + kk) * 2048, 16384, 1024), idesc,
+            accumulate || w > 0 || kk > 0);
+}
+
+// 128 x 128 scores of two K-major tiles over the head dim.
+template <int DH>
+__device__ __forceinline__ void grad_mma_scores(uint32_t d, uint32_t a_tile, uint32_t b_tile) {
+  constexpr uint32_t idesc = idesc_bf16(128, 128, false, false);
+#pragma unroll
+  for (int kk = 0; kk < DH / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+    umma_ss(d, sdesc_sw128(a_tile + off, 16, 1024), sdesc_sw128(b_tile + off, 16, 1024), idesc,
+            kk > 0);
+  }
+}
+
+// ---------------------------------------------------------------- key pass
+
+struct KeyPass {
+  int far_parts;      // 0: every tile walks all its queries
+  int far_tiles;      // tiles with sinks of a sequence, at most
+  float* far;         // [B, far_tiles, H_kv, far_parts, 2, DH, 128]
+  const float* nlse2;
+  const float* delta;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int64_t ld;
+};
+
+// The query tiles (128 queries, counted from the sequence's first) that see a
+// tile of keys [ks, ke]: `near` ones [n0, n1) and the far ones [n1, n2).
+struct KeyRange {
+  int n0, n1, n2;
+  __device__ void init(const SinkDims& s, const SinkSeq& seq, int ks, int ke) {
+    const int nq = seq.nq(), shift = seq.shift();
+    const int lo = max(0, ks - shift - s.m.ahead);
+    const int hi = min(nq, ke - shift + s.m.window);
+    n2 = (nq + 127) / 128;
+    n0 = min(lo / 128, n2);
+    n1 = max(n0, hi > 0 ? (hi + 127) / 128 : 0);
+    if (ks >= s.m.sinks) n2 = n1;
+  }
+};
+
+// Softmax part of the key pass: thread = key row, this warpgroup's 64 of the
+// tile's 128 queries.  TMEM columns: S^T [0, 128), dP^T [128, 256).
+template <int DH>
+__device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t* st_full,
+                                                 uint64_t* s_full, uint64_t* dp_full,
+                                                 uint64_t* p_ready, uint64_t* ds_ready,
+                                                 const uint8_t* stats, const SinkMask& m, int ks,
+                                                 int shift, int t0, int tiles, int i0, int i1,
+                                                 float scale_log2, uint64_t budget_ns) {
+  using Cfg = GradCfg<DH>;
+  const uint32_t quarter = warp_id() & 3;
+  const uint32_t lane_off = (quarter * 32) << 16;
+  const uint32_t s_addr = tmem + 64 * w + lane_off, dp_addr = s_addr + 128;
+  const int kw = ks + quarter * 32, key = kw + lane_id();
+  const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
+  for (int i = i0; i < i1; ++i) {
+    const int t = i - i0, s = t % Cfg::STAGES;
+    const int p0 = 128 * (t0 + i % tiles) + shift + 64 * w;  // position of this half's query 0
+    const bool edge = !sink_sees_all(m, p0, p0 + 63, kw, kw + 31);
+    const int c_lo = key - m.ahead - p0;                     // visible columns [c_lo, c_hi)
+    const int c_hi = key < m.sinks ? 64 : key - p0 + m.window;
+    if (!__all_sync(0xffffffffu, mbar_wait(&st_full[s], (t / Cfg::STAGES) & 1, budget_ns) &&
+                                     mbar_wait(s_full, t & 1, budget_ns)))
+      return false;
+    tc_fence_after();
+    const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(stats + s * Cfg::STATS) + 16 * w;
+    const ulonglong2* dl = nl + 32;
+    uint32_t x[64];
+    uint32_t (&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
+    uint32_t (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
+    tmem_ld32(s_addr, x0);
+    tmem_ld32(s_addr + 32, x1);
+    tmem_ld_wait();
+    reg_fence(x0);
+    reg_fence(x1);
+    // P over S in place: 2^(s scale log2 e - lse log2 e)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const ulonglong2 n2 = nl[e];
+      const uint64_t a = f32x2_fma((static_cast<uint64_t>(x[4 * e + 1]) << 32) | x[4 * e], cc, n2.x);
+      const uint64_t b =
+          f32x2_fma((static_cast<uint64_t>(x[4 * e + 3]) << 32) | x[4 * e + 2], cc, n2.y);
+      x[4 * e] = __float_as_uint(exp2_mufu(f32x2_lo(a)));
+      x[4 * e + 1] = __float_as_uint(exp2_mufu(f32x2_hi(a)));
+      x[4 * e + 2] = __float_as_uint(exp2_mufu(f32x2_lo(b)));
+      x[4 * e + 3] = __float_as_uint(exp2_mufu(f32x2_hi(b)));
+    }
+    if (edge) {
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        if (c < c_lo || c >= c_hi) x[c] = 0;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        pk[e] = pack_bf16x2(__uint_as_float(x[32 * q + 2 * e]),
+                            __uint_as_float(x[32 * q + 2 * e + 1]));
+      tmem_st16(s_addr + 16 * q, pk);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&p_ready[w]);
+    // dS = P (dP - D)
+    if (!__all_sync(0xffffffffu, mbar_wait(dp_full, t & 1, budget_ns))) return false;
+    tc_fence_after();
+    uint32_t ds[32];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t g[32];
+      tmem_ld32(dp_addr + 32 * q, g);
+      tmem_ld_wait();
+      reg_fence(g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const ulonglong2 d2 = dl[8 * q + e];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const uint64_t d = f ? d2.y : d2.x;
+          const int c = 4 * e + 2 * f;
+          float a = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - f32x2_lo(d));
+          float b = __uint_as_float(x[32 * q + c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d));
+          if (edge) {  // 0 x NaN of a hidden pair
+            if (32 * q + c < c_lo || 32 * q + c >= c_hi) a = 0.f;
+            if (32 * q + c + 1 < c_lo || 32 * q + c + 1 >= c_hi) b = 0.f;
+          }
+          ds[16 * q + 2 * e + f] = pack_bf16x2(a, b);
+        }
+      }
+    }
+    // both halves of dP^T are in registers before dS goes over them
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      tmem_st16(dp_addr + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&ds[16 * q]));
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&ds_ready[w]);
+  }
+  return true;
+}
+
+template <int DH, bool FAR>
+__global__ void __launch_bounds__(kThreads, 1)
+    sink_key_pass_kernel(const __grid_constant__ CUtensorMap qmap,
+                         const __grid_constant__ CUtensorMap domap,
+                         const __grid_constant__ CUtensorMap kmap,
+                         const __grid_constant__ CUtensorMap vmap, const SinkDims dims,
+                         const KeyPass a, float scale, uint32_t* status, uint64_t budget_ns) {
+  using Cfg = GradCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* kvbuf = smem;                   // K, V
+  uint8_t* ring = smem + 2 * Cfg::TILE;    // stage s: Q, dO
+  uint8_t* stats = ring + Cfg::STAGES * 2 * Cfg::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stats + Cfg::STAGES * Cfg::STATS);
+  uint64_t* kv_full = bars;
+  uint64_t* q_full = bars + 1;                  // [STAGES]
+  uint64_t* do_full = q_full + Cfg::STAGES;     // [STAGES]
+  uint64_t* st_full = do_full + Cfg::STAGES;    // [STAGES]
+  uint64_t* q_empty = st_full + Cfg::STAGES;    // [STAGES] Q and the statistics
+  uint64_t* do_empty = q_empty + Cfg::STAGES;   // [STAGES]
+  uint64_t* s_full = do_empty + Cfg::STAGES;
+  uint64_t* dp_full = s_full + 1;
+  uint64_t* p_ready = dp_full + 1;              // [2] one per warpgroup
+  uint64_t* ds_ready = p_ready + 2;             // [2]
+  uint64_t* mma_done = ds_ready + 2;
+  uint64_t* cut = mma_done + 1;                 // tiles whose last rows are zeroed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
+
+  // Ascending keys: without a window the first keys see the most queries.
+  const int lin = blockIdx.x;
+  const int hk = lin % dims.Hkv;
+  int b, tile, part = 0;
+  if (FAR) {
+    part = lin / dims.Hkv % a.far_parts;
+    const int t = lin / dims.Hkv / a.far_parts;
+    b = t / a.far_tiles;
+    tile = t % a.far_tiles;
+  } else {
+    const int slot = lin / dims.Hkv;
+    b = sink_slot_seq(dims.cu_k, dims.B, dims.Lk, 128, slot);
+    tile = slot - sink_slot_base(dims.cu_k, b, dims.Lk, 128);
+  }
+  const SinkSeq seq = sink_seq(dims, b);
+  const int ks = 128 * tile;
+  if (ks >= seq.nk() || (FAR && ks >= dims.m.sinks)) return;  // the whole CTA
+  const int ke = min(ks + 127, seq.nk() - 1);
+  const int key0 = seq.k0 + ks;
+  const int group = dims.H / dims.Hkv;
+  KeyRange kr;
+  kr.init(dims, seq, ks, ke);
+  const bool split = a.far_parts > 0 && kr.n2 > kr.n1;
+  const int far_items = split ? (kr.n2 - kr.n1) * group : 0;
+  // items: query tiles t0 .. t0 + tiles of each query head in turn
+  const int t0 = FAR ? kr.n1 : kr.n0;
+  const int tiles = (FAR || !split ? kr.n2 : kr.n1) - t0;
+  int i0 = 0, i1 = tiles * group;
+  auto far_begin = [&](int f) {
+    return static_cast<int>(static_cast<int64_t>(far_items) * f / a.far_parts);
+  };
+  if (FAR) {
+    i0 = far_begin(part);
+    i1 = far_begin(part + 1);
+    if (i0 >= i1) return;  // the reader leaves it out by the same arithmetic
+  }
+  const int items = i1 - i0;
+  const int q_base = sink_slot_base(dims.cu_q, b, dims.Lq, 128);
+  const int q_slots = sink_slots(dims.Lq, dims.B, 128);
+  const uint32_t warp = warp_id();
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&do_full[s], 1);
+      mbar_init(&st_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&do_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(dp_full, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&p_ready[w], 128);
+      mbar_init(&ds_ready[w], 128);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(cut, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&domap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t dv_addr = tmem + 256, dk_addr = tmem + 256 + DH;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+  }
+  if (warp == 0) {
+    // ================================================================ TMA
+    const bool leader = lane_id() == 0;
+    if (leader) {
+      mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE);
+      for (int sl = 0; sl < Cfg::SLABS; ++sl) {
+        tma_load_2d(kvbuf + sl * 16384, &kmap, kv_full, hk * DH + 64 * sl, key0);
+        tma_load_2d(kvbuf + Cfg::TILE + sl * 16384, &vmap, kv_full, hk * DH + 64 * sl, key0);
+      }
+    }
+    int issued = 0, cuts = 0;
+    bool ok = true;
+    for (int i = i0; i < i1; ++i) {
+      const int t = i - i0, s = t % Cfg::STAGES;
+      const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
+      const int qt = t0 + i % tiles, h = hk * group + i / tiles;
+      const int row = seq.q0 + 128 * qt, valid = min(128, seq.nq() - 128 * qt);
+      uint8_t* qb = ring + s * 2 * Cfg::TILE;
+      uint8_t* dob = qb + Cfg::TILE;
+      if (t >= Cfg::STAGES &&
+          !__all_sync(0xffffffffu, mbar_wait(&q_empty[s], par, budget_ns))) {
+        ok = false;
+        break;
+      }
+      uint64_t* qbar = valid < 128 ? cut : &q_full[s];
+      if (leader) {
+        mbar_arrive_expect_tx(&st_full[s], Cfg::STATS);
+        const int64_t at = (static_cast<int64_t>(h) * q_slots + q_base + qt) * 128;
+        bulk_load(stats + s * Cfg::STATS, a.nlse2 + at, 512, &st_full[s]);
+        bulk_load(stats + s * Cfg::STATS + 512, a.delta + at, 512, &st_full[s]);
+        mbar_arrive_expect_tx(qbar, (valid < 128 ? 2 : 1) * Cfg::TILE);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(qb + sl * 16384, &qmap, qbar, h * DH + 64 * sl, row);
+      }
+      __syncwarp();
+      ++issued;
+      if (t >= Cfg::STAGES &&
+          !__all_sync(0xffffffffu, mbar_wait(&do_empty[s], par, budget_ns))) {
+        ok = false;
+        break;
+      }
+      uint64_t* dobar = valid < 128 ? cut : &do_full[s];
+      if (leader) {
+        if (valid == 128) mbar_arrive_expect_tx(dobar, Cfg::TILE);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(dob + sl * 16384, &domap, dobar, h * DH + 64 * sl, row);
+      }
+      __syncwarp();
+      if (valid < 128) {
+        // queries past the sequence's end have P = 0; their rows must not
+        // be NaN
+        if (!__all_sync(0xffffffffu, mbar_wait(cut, cuts & 1, budget_ns))) {
+          ok = false;
+          break;
+        }
+        ++cuts;
+        sink_zero_rows(qb, Cfg::SLABS, valid);
+        sink_zero_rows(dob, Cfg::SLABS, valid);
+        if (leader) {
+          mbar_arrive(&q_full[s]);
+          mbar_arrive(&do_full[s]);
+        }
+      }
+    }
+    if (!ok) record_status(status, kStatusTimeout);
+    // no load may be in flight when the CTA ends
+    mbar_wait(kv_full, 0, 200000000ull);
+    for (int t = max(0, issued - Cfg::STAGES); t < issued; ++t) {
+      const uint32_t par = (t / Cfg::STAGES) & 1;
+      mbar_wait(&st_full[t % Cfg::STAGES], par, 200000000ull);
+      mbar_wait(&q_full[t % Cfg::STAGES], par, 200000000ull);
+      mbar_wait(&do_full[t % Cfg::STAGES], par, 200000000ull);
+    }
+    if (!ok) mbar_wait(cut, cuts & 1, 200000000ull);  // a cut tile's loads may be in flight
+  } else if (warp == 1) {
+    // ================================================================ MMA
+    if (elect_one()) {
+      const uint32_t kb = smem_u32(kvbuf), vb = kb + Cfg::TILE;
+      auto q_tile = [&](int t) { return smem_u32(ring) + t % Cfg::STAGES * 2 * Cfg::TILE; };
+      auto full = [&](uint64_t* bar, int t) {
+        if (!mbar_wait(&bar[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, budget_ns)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto scores = [&](int t) {  // S^T = K Q^T
+        if (!full(q_full, t)) return false;
+        grad_mma_scores<DH>(tmem, kb, q_tile(t));
+        umma_commit(s_full);
+        return true;
+      };
+      auto d_scores = [&](int t) {  // dP^T = V dO^T
+        if (!full(do_full, t)) return false;
+        grad_mma_scores<DH>(tmem + 128, vb, q_tile(t) + Cfg::TILE);
+        umma_commit(dp_full);
+        return true;
+      };
+      // dV += P^T dO or dK += dS^T Q, each half as its warpgroup is done
+      auto sums = [&](uint64_t* ready, uint32_t d, uint32_t at, uint32_t tile, int t) {
+        for (int w = 0; w < 2; ++w) {
+          if (!mbar_wait(&ready[w], t & 1, budget_ns)) return false;
+          tc_fence_after();
+          grad_mma_half<DH>(d, at, tile, w, t > 0);
+        }
+        return true;
+      };
+      bool ok = mbar_wait(kv_full, 0, budget_ns);
+      if (ok && items > 0) ok = scores(0) && d_scores(0);
+      // While the tensor core runs dV_t and S_{t+1}, the warpgroups form dS_t;
+      // while it runs dK_t and dP_{t+1}, they form P_{t+1}.
+      for (int t = 0; t < items && ok; ++t) {
+        ok = sums(p_ready, dv_addr, tmem, q_tile(t) + Cfg::TILE, t);
+        if (!ok) break;
+        umma_commit(&do_empty[t % Cfg::STAGES]);
+        if (t + 1 < items && !(ok = scores(t + 1))) break;
+        ok = sums(ds_ready, dk_addr, tmem + 128, q_tile(t), t);
+        if (!ok) break;
+        umma_commit(&q_empty[t % Cfg::STAGES]);
+        if (t + 1 < items) ok = d_scores(t + 1);
+      }
+      if (!ok) record_status(status, kStatusTimeout);
+      umma_commit(mma_done);
+    }
+  } else if (warp >= 4) {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    const int w = (warp - 4) >> 2;
+    const bool ok = key_pass_softmax<DH>(w, tmem, st_full, s_full, dp_full, p_ready, ds_ready,
+                                         stats, dims.m, ks, seq.shift(), t0, tiles, i0, i1,
+                                         scale * 1.4426950408889634f, budget_ns);
+    // warpgroup 0 stores dV, warpgroup 1 dK
+    if (__all_sync(0xffffffffu, ok && mbar_wait(mma_done, 0, budget_ns))) {
+      tc_fence_after();
+      const int row = (warp & 3) * 32 + lane_id();
+      const uint32_t addr = (w ? dk_addr : dv_addr) + (((warp & 3) * 32) << 16);
+      const float factor = w ? scale : 1.f;
+      const int64_t far_at =
+          (((static_cast<int64_t>(b) * a.far_tiles + tile) * dims.Hkv + hk) * a.far_parts) * 2 + w;
+      __nv_bfloat16* dst = (w ? a.dk : a.dv) + static_cast<int64_t>(key0 + row) * a.ld + hk * DH;
+      const bool live = ks + row <= ke && in_bounds(status, key0 + row, dims.Lk, hk * DH, DH,
+                                                    static_cast<int64_t>(dims.Hkv) * DH);
+#pragma unroll 1
+      for (int c = 0; c < DH; c += 32) {
+        uint32_t x[32];
+        if (items > 0) {
+          tmem_ld32(addr + c, x);
+          tmem_ld_wait();
+          reg_fence(x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0;
+        }
+        if (FAR) {
+          float* out = a.far + (far_at + 2 * part) * (DH * 128) + c * 128 + row;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) out[e * 128] = __uint_as_float(x[e]);
+          continue;
+        }
+        if (split) {
+          for (int f = 0; f < a.far_parts; ++f) {
+            if (far_begin(f) >= far_begin(f + 1)) continue;
+            const float* in = a.far + (far_at + 2 * f) * (DH * 128) + c * 128 + row;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = __float_as_uint(__uint_as_float(x[e]) + in[e * 128]);
+          }
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint4 u;
+          auto two = [&](int n) {
+            return pack_bf16x2(__uint_as_float(x[e + n]) * factor,
+                               __uint_as_float(x[e + n + 1]) * factor);
+          };
+          u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
+          *reinterpret_cast<uint4*>(dst + c + e) = u;
+        }
+      }
+    } else {
+      record_status(status, kStatusTimeout);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    mbar_wait(mma_done, 0, 200000000ull);
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- query pass
+//
+// A CTA holds 128 queries of one head (Q and dO resident) and walks the key
+// tiles they see.  TMEM columns: S [0, 128), dP twice [128, 384), dQ
+// [384, 384 + DH): S_{j+1} is issued once the warpgroups have loaded S_j, dP
+// alternates, so both are ready when the warpgroups come back for them.
+template <int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    sink_query_pass_kernel(const __grid_constant__ CUtensorMap qmap,
+                           const __grid_constant__ CUtensorMap domap,
+                           const __grid_constant__ CUtensorMap kmap,
+                           const __grid_constant__ CUtensorMap vmap, const SinkDims dims,
+                           const float* __restrict__ nlse2, const float* __restrict__ delta,
+                           float scale, __nv_bfloat16* __restrict__ dq, int64_t ld_dq,
+                           uint32_t* status, uint64_t budget_ns) {
+  using Cfg = GradCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* qbuf = smem;                  // Q, dO
+  uint8_t* ring = smem + 2 * Cfg::TILE;  // stage s: K, V
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + Cfg::STAGES * 2 * Cfg::TILE);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;                // [STAGES]
+  uint64_t* v_full = k_full + Cfg::STAGES;    // [STAGES]
+  uint64_t* k_empty = v_full + Cfg::STAGES;   // [STAGES]
+  uint64_t* v_empty = k_empty + Cfg::STAGES;  // [STAGES]
+  uint64_t* s_full = v_empty + Cfg::STAGES;
+  uint64_t* s_free = s_full + 1;              // S loaded by all 256 threads
+  uint64_t* dp_full = s_free + 1;             // [2]
+  uint64_t* ds_ready = dp_full + 2;           // [2] one per warpgroup
+  uint64_t* mma_done = ds_ready + 2;
+  uint64_t* cut = mma_done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
+
+  // Heaviest first: the last queries of a sequence see the most keys.
+  const int slots = sink_slots(dims.Lq, dims.B, 128);
+  const int slot = slots - 1 - static_cast<int>(blockIdx.x) / dims.H;
+  const int h = static_cast<int>(blockIdx.x) % dims.H, hk = h / (dims.H / dims.Hkv);
+  const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
+  const SinkSeq seq = sink_seq(dims, b);
+  const int row0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
+  if (row0 >= seq.q1) return;  // the whole CTA
+  const int pa = row0 - seq.q0 + seq.shift(), pb = min(pa + 127, seq.nk() - 1);
+  SinkKeyTiles kt;
+  kt.init(dims.m, pa, pb, seq.nk());
+  const uint32_t warp = warp_id();
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 256);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&dp_full[w], 1);
+      mbar_init(&ds_ready[w], 128);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(cut, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&qmap);
+    tma_prefetch_desc(&domap);
+    tma_prefetch_desc(&kmap);
+    tma_prefetch_desc(&vmap);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t dq_addr = tmem + 384;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+  }
+  if (warp == 0) {
+    // ================================================================ TMA
+    const bool leader = lane_id() == 0;
+    if (leader) {
+      mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE);
+      for (int sl = 0; sl < Cfg::SLABS; ++sl) {
+        tma_load_2d(qbuf + sl * 16384, &qmap, q_full, h * DH + 64 * sl, row0);
+        tma_load_2d(qbuf + Cfg::TILE + sl * 16384, &domap, q_full, h * DH + 64 * sl, row0);
+      }
+    }
+    int issued_k = 0, issued_v = 0, cuts = 0;
+    bool ok = true;
+    for (int j = 0; j < kt.n; ++j) {
+      const int s = j % Cfg::STAGES;
+      const uint32_t par = ((j / Cfg::STAGES) & 1) ^ 1;
+      const int key0 = seq.k0 + kt.start(j), valid = kt.valid(j);
+      uint8_t* kb = ring + s * 2 * Cfg::TILE;
+      uint8_t* vb = kb + Cfg::TILE;
+      if (j >= Cfg::STAGES && !__all_sync(0xffffffffu, mbar_wait(&v_empty[s], par, budget_ns))) {
+        ok = false;
+        break;
+      }
+      if (leader) {
+        mbar_arrive_expect_tx(&v_full[s], Cfg::TILE);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(vb + sl * 16384, &vmap, &v_full[s], hk * DH + 64 * sl, key0);
+      }
+      __syncwarp();
+      ++issued_v;
+      if (j >= Cfg::STAGES && !__all_sync(0xffffffffu, mbar_wait(&k_empty[s], par, budget_ns))) {
+        ok = false;
+        break;
+      }
+      uint64_t* full = valid < 128 ? cut : &k_full[s];
+      if (leader) {
+        mbar_arrive_expect_tx(full, Cfg::TILE);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(kb + sl * 16384, &kmap, full, hk * DH + 64 * sl, key0);
+      }
+      __syncwarp();
+      if (valid < 128) {
+        if (!__all_sync(0xffffffffu, mbar_wait(cut, cuts & 1, budget_ns))) {
+          ok = false;
+          break;
+        }
+        ++cuts;
+        sink_zero_rows(kb, Cfg::SLABS, valid);
+        if (leader) mbar_arrive(&k_full[s]);
+      }
+      ++issued_k;
+    }
+    if (!ok) record_status(status, kStatusTimeout);
+    mbar_wait(q_full, 0, 200000000ull);
+    for (int t = max(0, issued_v - Cfg::STAGES); t < issued_v; ++t)
+      mbar_wait(&v_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
+    for (int t = max(0, issued_k - Cfg::STAGES); t < issued_k; ++t)
+      mbar_wait(&k_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
+    if (!ok) mbar_wait(cut, cuts & 1, 200000000ull);  // a cut tile's load may be in flight
+  } else if (warp == 1) {
+    // ================================================================ MMA
+    if (elect_one()) {
+      const uint32_t qb = smem_u32(qbuf), dob = qb + Cfg::TILE;
+      auto k_tile = [&](int j) { return smem_u32(ring) + j % Cfg::STAGES * 2 * Cfg::TILE; };
+      auto products = [&](int j) {  // S = Q K^T and dP = dO V^T
+        const int s = j % Cfg::STAGES;
+        if (!mbar_wait(&k_full[s], (j / Cfg::STAGES) & 1, budget_ns)) return false;
+        tc_fence_after();
+        grad_mma_scores<DH>(tmem, qb, k_tile(j));
+        umma_commit(s_full);
+        if (!mbar_wait(&v_full[s], (j / Cfg::STAGES) & 1, budget_ns)) return false;
+        tc_fence_after();
+        grad_mma_scores<DH>(tmem + 128 + 128 * (j & 1), dob, k_tile(j) + Cfg::TILE);
+        umma_commit(&dp_full[j & 1]);
+        umma_commit(&v_empty[s]);
+        return true;
+      };
+      bool ok = mbar_wait(q_full, 0, budget_ns);
+      if (ok && kt.n > 0) ok = products(0);
+      for (int j = 0; j < kt.n && ok; ++j) {
+        if (j + 1 < kt.n) {
+          if (!(ok = mbar_wait(s_free, j & 1, budget_ns))) break;
+          tc_fence_after();
+          if (!(ok = products(j + 1))) break;
+        }
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (!(ok = mbar_wait(&ds_ready[w], j & 1, budget_ns))) break;
+          tc_fence_after();
+          grad_mma_half<DH>(dq_addr, tmem + 128 + 128 * (j & 1), k_tile(j), w, j > 0);
+        }
+        if (ok) umma_commit(&k_empty[j % Cfg::STAGES]);
+      }
+      if (!ok) record_status(status, kStatusTimeout);
+      umma_commit(mma_done);
+    }
+  } else if (warp >= 4) {
+    // ================================================================ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    const int w = (warp - 4) >> 2;           // this warpgroup's 64 keys of a tile
+    const uint32_t quarter = warp & 3;
+    const uint32_t lane_off = (quarter * 32) << 16;
+    const int row = quarter * 32 + lane_id();
+    const int p = pa + row, pw = pa + quarter * 32;
+    const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + row;
+    const float nl = nlse2[at], dl = delta[at];
+    const float scale_log2 = scale * 1.4426950408889634f;
+    const SinkMask m = dims.m;
+    bool ok = true;
+    for (int j = 0; j < kt.n; ++j) {
+      const int ks = kt.start(j) + 64 * w, valid = kt.valid(j) - 64 * w;
+      const bool edge = valid < 64 || !sink_sees_all(m, pw, pw + 31, ks, ks + 63);
+      const int c_end = min(valid, p + m.ahead + 1 - ks);
+      const int c_win = p - m.window + 1 - ks, c_sink = m.sinks - ks;
+      if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, budget_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t x[64];
+      uint32_t (&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
+      uint32_t (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
+      tmem_ld32(tmem + lane_off + 64 * w, x0);
+      tmem_ld32(tmem + lane_off + 64 * w + 32, x1);
+      tmem_ld_wait();
+      reg_fence(x0);
+      reg_fence(x1);
+      tc_fence_before();
+      mbar_arrive(s_free);
+#pragma unroll
+      for (int c = 0; c < 64; ++c)
+        x[c] = __float_as_uint(exp2_mufu(fmaf(__uint_as_float(x[c]), scale_log2, nl)));
+      if (!__all_sync(0xffffffffu, mbar_wait(&dp_full[j & 1], (j >> 1) & 1, budget_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t g_addr = tmem + 128 + 128 * (j & 1) + 64 * w + lane_off;
+      uint32_t ds[32];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t g[32];
+        tmem_ld32(g_addr + 32 * q, g);
+        tmem_ld_wait();
+        reg_fence(g);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float v = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - dl);
+          if (edge && (32 * q + c >= c_end || (32 * q + c < c_win && 32 * q + c >= c_sink)))
+            v = 0.f;
+          g[c] = __float_as_uint(v);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          ds[16 * q + e] = pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        tmem_st16(g_addr + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&ds[16 * q]));
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&ds_ready[w]);
+    }
+    if (__all_sync(0xffffffffu, ok && mbar_wait(mma_done, 0, budget_ns))) {
+      tc_fence_after();
+      const bool live = row0 + row < seq.q1 &&
+                        in_bounds(status, row0 + row, dims.Lq, h * DH, DH,
+                                  static_cast<int64_t>(dims.H) * DH);
+      __nv_bfloat16* dst = dq + static_cast<int64_t>(row0 + row) * ld_dq + h * DH;
+      // each warpgroup stores half the columns
+#pragma unroll 1
+      for (int c = w * (DH / 2); c < (w + 1) * (DH / 2); c += 32) {
+        uint32_t x[32];
+        if (kt.n > 0) {
+          tmem_ld32(dq_addr + lane_off + c, x);
+          tmem_ld_wait();
+          reg_fence(x);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = 0;
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint4 u;
+          auto two = [&](int n) {
+            return pack_bf16x2(__uint_as_float(x[e + n]) * scale,
+                               __uint_as_float(x[e + n + 1]) * scale);
+          };
+          u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
+          *reinterpret_cast<uint4*>(dst + c + e) = u;
+        }
+      }
+    } else {
+      record_status(status, kStatusTimeout);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    mbar_wait(mma_done, 0, 200000000ull);
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+// Far parts: only where sequences can be more than twice as long as what a
+// plain key tile walks, and the tiles with sinks alone leave SMs idle; then
+// about two CTAs an SM over all of them, eight query tiles at least each.
+struct FarPlan {
+  int parts, tiles;
+};
+
+FarPlan far_plan(const vdn_sink_shape& s) {
+  FarPlan f{0, 0};
+  const int longest = s.Lq < s.Lk ? s.Lq : s.Lk;
+  if (s.sinks == 0 || longest == 0) return f;
+  const int sinks = s.sinks < s.Lk ? s.sinks : s.Lk;
+  f.tiles = (sinks + 127) / 128;
+  const int64_t owners = static_cast<int64_t>(s.B) * f.tiles * s.H_kv;
+  if (static_cast<int64_t>(s.Lq) <= 2 * (static_cast<int64_t>(s.window) + s.ahead + 256) ||
+      owners >= 148)
+    return FarPlan{0, 0};
+  const int64_t most = static_cast<int64_t>(s.Lq) / 128 * (s.H / s.H_kv) / 8;
+  int64_t n = 2 * 148 / owners;
+  n = n > most ? most : n;
+  n = n > 32 ? 32 : n;
+  f.parts = n < 1 ? 0 : static_cast<int>(n);
+  return f;
+}
+
+struct GradLayout {
+  size_t stats;  // bytes of one statistic
+  FarPlan far;
+  size_t total;
+};
+
+GradLayout grad_layout(const vdn_sink_shape& s) {
+  GradLayout l;
+  l.stats = static_cast<size_t>(s.H) * sink_slots(s.Lq, s.B, 128) * 128 * sizeof(float);
+  l.far = far_plan(s);
+  l.total = kStatusBytes + 2 * l.stats +
+            static_cast<size_t>(s.B) * l.far.tiles * s.H_kv * l.far.parts * 2 * s.d * 128 *
+                sizeof(float);
+  return l;
+}
+
+struct GradMaps {
+  CUtensorMap q, d_o, k, v;
+};
+
+template <int DH>
+cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const GradMaps& t,
+                             const FarPlan& far, KeyPass a, const __nv_bfloat16* o, int64_t ld_o,
+                             const __nv_bfloat16* d_o, int64_t ld_do, const float* lse,
+                             float* nlse2, float* delta, float scale, __nv_bfloat16* dq,
+                             int64_t ld_dq) {
+  using Cfg = GradCfg<DH>;
+  static std::atomic<uint64_t> set_near{0}, set_far{0}, set_query{0};
+  if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, false>, Cfg::SMEM, set_near)) return e;
+  if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, true>, Cfg::SMEM, set_far)) return e;
+  if (cudaError_t e = set_smem_once(sink_query_pass_kernel<DH>, Cfg::SMEM, set_query)) return e;
+  const int q_slots = sink_slots(dims.Lq, dims.B, 128);
+  if (dims.Lq > 0) {
+    sink_stats_kernel<<<4 * q_slots, 256, 0, ctx.stream>>>(dims, DH, o, ld_o, d_o, ld_do, lse,
+                                                           nlse2, delta);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  if (far.parts > 0) {
+    sink_key_pass_kernel<DH, true>
+        <<<dims.B * far.tiles * dims.Hkv * far.parts, kThreads, Cfg::SMEM, ctx.stream>>>(
+            t.q, t.d_o, t.k, t.v, dims, a, scale, ctx.status, ctx.budget_ns);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  if (dims.Lk > 0) {
+    sink_key_pass_kernel<DH, false><<<sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, kThreads,
+                                      Cfg::SMEM, ctx.stream>>>(t.q, t.d_o, t.k, t.v, dims, a,
+                                                               scale, ctx.status, ctx.budget_ns);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
+  if (dims.Lq > 0)
+    sink_query_pass_kernel<DH><<<q_slots * dims.H, kThreads, Cfg::SMEM, ctx.stream>>>(
+        t.q, t.d_o, t.k, t.v, dims, nlse2, delta, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+}  // namespace vdn
+
+using namespace vdn;
+
+extern "C" {
+
+size_t vdn_sink_attn_backward_workspace(const vdn_sink_shape* shape) {
+  vdn_sink_shape s;
+  const void* p = reinterpret_cast<const void*>(256);
+  if (shape == nullptr ||
+      sink_check(shape, p, (int64_t)1 << 24, p, p, (int64_t)1 << 24,
+                 static_cast<const int32_t*>(p), static_cast<const int32_t*>(p), &s) != VDN_OK)
+    return 0;
+  return grad_layout(s).total;
+}
+
+vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, int64_t ld_q,
+                                  const void* k, const void* v, int64_t ld_kv,
+                                  const int32_t* cu_q, const int32_t* cu_k, float scale,
+                                  const void* o, int64_t ld_o, const float* lse, const void* d_o,
+                                  int64_t ld_do, void* dq, int64_t ld_dq, void* dk, void* dv,
+                                  int64_t ld_dkv, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx("vdn_sink_attn_backward");
+  vdn_sink_shape s;
+  const vdn_status r = sink_check(shape, q, ld_q, k, v, ld_kv, cu_q, cu_k, &s);
+  if (r != VDN_OK) return r;
+  const int64_t D = static_cast<int64_t>(s.H) * s.d, Dk = static_cast<int64_t>(s.H_kv) * s.d;
+  auto bad = [](const void* p, int rows, int64_t ld, int64_t cols) {
+    return (p == nullptr && rows > 0) || (reinterpret_cast<uintptr_t>(p) & 15u) || ld < cols ||
+           ld % 8 != 0;
+  };
+  if (bad(o, s.Lq, ld_o, D) || bad(d_o, s.Lq, ld_do, D) || bad(dq, s.Lq, ld_dq, D) ||
+      bad(dk, s.Lk, ld_dkv, Dk) || bad(dv, s.Lk, ld_dkv, Dk) || (lse == nullptr && s.Lq > 0) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return VDN_ERR_INVALID_ARG;
+  const GradLayout lay = grad_layout(s);
+  if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < lay.total)
+    return VDN_ERR_WORKSPACE;
+  const int64_t limit = int64_t(1) << 31;
+  if (static_cast<int64_t>(sink_slots(s.Lq, s.B, 128)) * s.H >= limit ||
+      static_cast<int64_t>(sink_slots(s.Lk, s.B, 128)) * s.H_kv >= limit ||
+      (static_cast<int64_t>(s.Lq) + 127) / 128 * (s.H / s.H_kv) >= limit)
+    return VDN_ERR_UNSUPPORTED;
+  if (s.Lq == 0 && s.Lk == 0) return VDN_OK;
+  const SinkDims dims{s.Lq, s.Lk, s.B, s.H, s.H_kv, cu_q, cu_k, {s.window, s.ahead, s.sinks}};
+  GradMaps t;
+  // without queries or keys the missing side's tiles are never loaded
+  if (s.Lq > 0 && (!make_rows_map(&t.q, q, D, ld_q, s.Lq, 128) ||
+                   !make_rows_map(&t.d_o, d_o, D, ld_do, s.Lq, 128)))
+    return VDN_ERR_CUDA;
+  if (s.Lk > 0 && (!make_rows_map(&t.k, k, Dk, ld_kv, s.Lk, 128) ||
+                   !make_rows_map(&t.v, v, Dk, ld_kv, s.Lk, 128)))
+    return VDN_ERR_CUDA;
+  if (s.Lq == 0) t.q = t.d_o = t.k;
+  if (s.Lk == 0) t.k = t.v = t.q;
+  uint8_t* base = static_cast<uint8_t*>(ws) + kStatusBytes;
+  float* nlse2 = reinterpret_cast<float*>(base);
+  float* delta = reinterpret_cast<float*>(base + lay.stats);
+  KeyPass a{lay.far.parts,
+            lay.far.tiles,
+            reinterpret_cast<float*>(base + 2 * lay.stats),
+            nlse2,
+            delta,
+            static_cast<__nv_bfloat16*>(dk),
+            static_cast<__nv_bfloat16*>(dv),
+            ld_dkv};
+  const Launch ctx{static_cast<cudaStream_t>(stream), static_cast<uint32_t*>(ws),
+                   current_wait_budget_ns()};
+  const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
+  auto run = [&](auto dh) {
+    return launch_sink_grad<decltype(dh)::value>(
+        ctx, dims, t, lay.far, a, static_cast<const __nv_bfloat16*>(o), ld_o,
+        static_cast<const __nv_bfloat16*>(d_o), ld_do, lse, nlse2, delta, sc,
+        static_cast<__nv_bfloat16*>(dq), ld_dq);
+  };
+  const cudaError_t e = s.d == 128 ? run(std::integral_constant<int, 128>{})
+                                   : run(std::integral_constant<int, 64>{});
+  return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -35,7 +35,8 @@ EXPORTS = ["vdn_vda_scan_workspace", "vdn_vda_scan", "vdn_vda_debug_buffers",
            "vdn_window_attn_mxfp8_workspace", "vdn_window_attn_mxfp8", "vdn_copy2d_async",
            "vdn_debug_bounds_enabled", "vdn_selftest_bounds", "vdn_rope", "vdn_qk_norm_rope",
            "vdn_qk_norm_rope_backward_workspace", "vdn_qk_norm_rope_backward",
-           "vdn_sink_attn_workspace", "vdn_sink_attn"]
+           "vdn_sink_attn_workspace", "vdn_sink_attn", "vdn_sink_attn_backward_workspace",
+           "vdn_sink_attn_backward"]
 
 SOLVER_CHOLESKY = 0
 SOLVER_GAUSS_JORDAN = 1
@@ -176,6 +177,11 @@ def lib():
     L.vdn_sink_attn.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P, _I64, _P,
                                 _P, _SZ, _P]
     L.vdn_sink_attn.restype = ctypes.c_int
+    L.vdn_sink_attn_backward_workspace.argtypes = [K]
+    L.vdn_sink_attn_backward_workspace.restype = _SZ
+    L.vdn_sink_attn_backward.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P,
+                                         _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _SZ, _P]
+    L.vdn_sink_attn_backward.restype = ctypes.c_int
     L.vdn_version.argtypes = []
     L.vdn_version.restype = ctypes.c_char_p
     _lib = L
@@ -891,6 +897,40 @@ def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=Non
                                _ptr(cu_q), _ptr(cu_k), float(scale), _ptr(out), _ld(out),
                                _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "vdn_sink_attn")
     return out, ws
+
+
+def sink_attn_backward_workspace(Lq, Lk, B, H, H_kv, d, window, sinks=0, ahead=0):
+    return int(lib().vdn_sink_attn_backward_workspace(
+        ctypes.byref(_sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead))))
+
+
+def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None,
+                       cu_k=None, scale=0.0, dq=None, dk=None, dv=None, ws=None, stream=None):
+    """Gradients of sink_attn, given its inputs, its o and lse and d_o =
+    dLoss/do.  Returns (dq, dk, dv, ws)."""
+    _same_device(q, k, v, o, lse, d_o, cu_q, cu_k, dq, dk, dv, ws)
+    shape = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k)
+    Lq, Lk, dev = q.shape[0], k.shape[0], q.device
+    if lse.dtype != torch.float32 or lse.shape != (H, Lq) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous fp32 [H, Lq]")
+    # rows of no sequence are not written: they start as zeros
+    new = torch.empty if cu_q is None else torch.zeros
+    dq = new((Lq, H * d), dtype=torch.bfloat16, device=dev) if dq is None else dq
+    dk = new((Lk, H_kv * d), dtype=torch.bfloat16, device=dev) if dk is None else dk
+    dv = new((Lk, H_kv * d), dtype=torch.bfloat16, device=dev) if dv is None else dv
+    for name, t, heads, rows in (("o", o, H, Lq), ("d_o", d_o, H, Lq), ("dq", dq, H, Lq),
+                                 ("dk", dk, H_kv, Lk), ("dv", dv, H_kv, Lk)):
+        _rows2d(name, t, heads * d, torch.bfloat16, rows)
+    if _ld(dk) != _ld(dv):
+        raise ValueError("dk and dv must share one row stride")
+    if ws is None:
+        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(ctypes.byref(shape))), dev)
+    _check(lib().vdn_sink_attn_backward(
+        ctypes.byref(shape), _ptr(q), _ld(q), _ptr(k), _ptr(v), _ld(k), _ptr(cu_q), _ptr(cu_k),
+        float(scale), _ptr(o), _ld(o), _ptr(lse), _ptr(d_o), _ld(d_o), _ptr(dq), _ld(dq),
+        _ptr(dk), _ptr(dv), _ld(dk), _ptr(ws), ws.numel(), _stream(stream)),
+        "vdn_sink_attn_backward")
+    return dq, dk, dv, ws
 
 
 # ---------------------------------------------------------------- full layer
