@@ -542,6 +542,35 @@ VDN_API vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const voi
                                           void* dv, int64_t ld_dkv, void* ws, size_t ws_bytes,
                                           void* stream);
 
+/* One new token per sequence of a causal stream with a sliding window and
+ * sinks: vdn_sink_attn with ahead = 0 for the last query of each sequence, over
+ * a rolling cache that holds only what it sees.
+ *
+ * Sequence b's cache has sinks + window slots; position p (counted from 0)
+ * lives in slot p while p < sinks + window, and in slot
+ * sinks + (p - sinks) mod window after that.  The call writes k_new, v_new of
+ * position positions[b] into their slot, and returns
+ *     o = softmax over the live slots of (scale q . k) v.
+ * The caller advances positions, one call a token; slots below
+ * min(positions[b], sinks + window) have to hold the earlier tokens, slots
+ * past them are not read.  A cache filled by a prefill holds position p's key
+ * at that same slot.
+ *
+ * q, o     : [B, ld] bf16, H heads;  k_new, v_new: [B, ld_new] bf16, H_kv heads
+ * k_cache, v_cache: bf16, slot s of sequence b at b * batch_stride +
+ *            s * ld_cache elements (no two sequences may share a cache)
+ * positions: device int32 [B]; a negative one marks an inactive sequence:
+ *            its cache and its row of o stay as they are
+ * scale    : <= 0 selects 1/sqrt(d)
+ * d 64 or 128, window >= 1.  B may be 0.  No workspace; one launch; the same
+ * call gives the same bits, and may be repeated for the same positions. */
+VDN_API vdn_status vdn_sink_attn_step(int B, int H, int H_kv, int d, int window, int sinks,
+                                      const void* q, int64_t ld_q, const void* k_new,
+                                      const void* v_new, int64_t ld_new, void* k_cache,
+                                      void* v_cache, int64_t ld_cache, int64_t batch_stride,
+                                      const int32_t* positions, float scale, void* o,
+                                      int64_t ld_o, void* stream);
+
 /* ------------------------------------------------------------------------
  * Status and diagnostics.
  * ------------------------------------------------------------------------ */

@@ -159,3 +159,21 @@ def test_bad_gradient_shapes_are_refused_on_the_host(L, change, code):
     assert lib.vdn_sink_attn_backward(
         ctypes.byref(s), P(A), 512, P(A), P(A), 256, None, None, 0.0, P(A), 512, P(A), P(A), 512,
         P(A), 512, P(A), P(A), 256, P(A), 1 << 40, None) == code
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(B=-1), 1), (dict(H=0), 1), (dict(H=3), 1), (dict(H_kv=0), 1), (dict(d=32), 2),
+    (dict(window=0), 1), (dict(sinks=-1), 1), (dict(window=1 << 30), 1), (dict(B=70000), 2),
+    (dict(q=0), 1), (dict(k_new=A + 8), 1), (dict(k_cache=0), 1), (dict(positions=0), 1),
+    (dict(positions=A + 2), 1), (dict(o=0), 1), (dict(ld_q=500), 1), (dict(ld_new=128), 1),
+    (dict(ld_cache=252), 1), (dict(ld_cache=128), 1), (dict(batch_stride=68 * 256 - 8), 1),
+    (dict(batch_stride=68 * 256 + 4), 1), (dict(B=0, q=0), 0)])
+def test_bad_step_arguments_are_refused_on_the_host(L, change, code):
+    lib, P = L.lib(), ctypes.c_void_p
+    a = dict(B=2, H=4, H_kv=2, d=128, window=64, sinks=4, q=A, ld_q=512, k_new=A, ld_new=256,
+             k_cache=A, ld_cache=256, batch_stride=68 * 256, positions=A, o=A)
+    a.update(change)
+    assert lib.vdn_sink_attn_step(
+        a["B"], a["H"], a["H_kv"], a["d"], a["window"], a["sinks"], P(a["q"]), a["ld_q"],
+        P(a["k_new"]), P(A), a["ld_new"], P(a["k_cache"]), P(A), a["ld_cache"],
+        a["batch_stride"], P(a["positions"]), 0.0, P(a["o"]), 512, None) == code

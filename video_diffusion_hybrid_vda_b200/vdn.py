@@ -36,7 +36,7 @@ EXPORTS = ["vdn_vda_scan_workspace", "vdn_vda_scan", "vdn_vda_debug_buffers",
            "vdn_debug_bounds_enabled", "vdn_selftest_bounds", "vdn_rope", "vdn_qk_norm_rope",
            "vdn_qk_norm_rope_backward_workspace", "vdn_qk_norm_rope_backward",
            "vdn_sink_attn_workspace", "vdn_sink_attn", "vdn_sink_attn_backward_workspace",
-           "vdn_sink_attn_backward"]
+           "vdn_sink_attn_backward", "vdn_sink_attn_step"]
 
 SOLVER_CHOLESKY = 0
 SOLVER_GAUSS_JORDAN = 1
@@ -182,6 +182,9 @@ def lib():
     L.vdn_sink_attn_backward.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P,
                                          _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _SZ, _P]
     L.vdn_sink_attn_backward.restype = ctypes.c_int
+    L.vdn_sink_attn_step.argtypes = [ctypes.c_int] * 6 + [_P, _I64, _P, _P, _I64, _P, _P, _I64,
+                                                          _I64, _P, ctypes.c_float, _P, _I64, _P]
+    L.vdn_sink_attn_step.restype = ctypes.c_int
     L.vdn_version.argtypes = []
     L.vdn_version.restype = ctypes.c_char_p
     _lib = L
@@ -931,6 +934,43 @@ def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=
         _ptr(dk), _ptr(dv), _ld(dk), _ptr(ws), ws.numel(), _stream(stream)),
         "vdn_sink_attn_backward")
     return dq, dk, dv, ws
+
+
+def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, window, sinks=0,
+                   scale=0.0, out=None, stream=None):
+    """One new token per sequence over a rolling cache of sinks + window slots.
+
+    q [B, H*d], k_new and v_new [B, H_kv*d] bf16; k_cache, v_cache
+    [B, sinks + window, H_kv*d] bf16, updated in place: position p's key lives
+    in slot p while p < sinks + window, then in slot sinks + (p - sinks) %
+    window.  positions: int32 [B], the new tokens' (negative: inactive, its
+    cache and row of ``out`` stay as they are).  Returns o [B, H*d]."""
+    _same_device(q, k_new, v_new, k_cache, v_cache, positions, out)
+    B = q.shape[0]
+    _rows2d("q", q, H * d, torch.bfloat16)
+    _rows2d("k_new", k_new, H_kv * d, torch.bfloat16, B)
+    _rows2d("v_new", v_new, H_kv * d, torch.bfloat16, B)
+    if _ld(k_new) != _ld(v_new):
+        raise ValueError("k_new and v_new must share one row stride")
+    shape = (B, int(sinks) + int(window), H_kv * d)
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dtype != torch.bfloat16 or c.shape != shape or (B and c.stride(2) != 1):
+            raise ValueError(f"{name}: bf16 {list(shape)} with contiguous columns")
+    if k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must share their strides")
+    if positions.dtype != torch.int32 or positions.shape != (B,) or \
+            not positions.is_contiguous():
+        raise ValueError("positions: contiguous int32 [B]")
+    if out is None:
+        out = torch.empty((B, H * d), dtype=torch.bfloat16, device=q.device)
+    _rows2d("out", out, H * d, torch.bfloat16, B)
+    ld_cache = k_cache.stride(1) if shape[1] > 1 else max(k_cache.stride(1), shape[2])
+    _check(lib().vdn_sink_attn_step(
+        B, int(H), int(H_kv), int(d), int(window), int(sinks), _ptr(q), _ld(q), _ptr(k_new),
+        _ptr(v_new), _ld(k_new), _ptr(k_cache), _ptr(v_cache), ld_cache, k_cache.stride(0),
+        _ptr(positions), float(scale), _ptr(out), _ld(out), _stream(stream)),
+        "vdn_sink_attn_step")
+    return out
 
 
 # ---------------------------------------------------------------- full layer
