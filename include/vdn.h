@@ -500,8 +500,11 @@ VDN_API vdn_status vdn_qk_norm_rope_backward(
  * q, o   : [Lq, ld] bf16;  k, v: [Lk, ld_kv] bf16
  * cu_q, cu_k: device int32 [B + 1], the first row of each sequence and the
  *          end of the last, ascending; NULL for one sequence of all rows
- *          (B = 1).  Rows that belong to no sequence are neither read into a
- *          result nor written.  Values outside [0, L] are clamped.
+ *          (B = 1).  Rows that belong to no sequence (before the first, from
+ *          the last end on) never reach a result.  Values outside [0, L] are
+ *          clamped.
+ * zero_rest: 0: the rows of o and lse of no sequence stay as they are;
+ *          non-zero: those of o are zeroed
  * scale  : <= 0 selects 1/sqrt(d)
  * lse_opt: NULL, or fp32 [H, Lq]: natural-log sum of exp(scaled scores)
  * ws     : >= vdn_sink_attn_workspace(shape) bytes
@@ -520,15 +523,17 @@ VDN_API size_t vdn_sink_attn_workspace(const vdn_sink_shape* shape);
 VDN_API vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_q,
                                  const void* k, const void* v, int64_t ld_kv,
                                  const int32_t* cu_q, const int32_t* cu_k, float scale, void* o,
-                                 int64_t ld_o, float* lse_opt, void* ws, size_t ws_bytes,
-                                 void* stream);
+                                 int64_t ld_o, int zero_rest, float* lse_opt, void* ws,
+                                 size_t ws_bytes, void* stream);
 
 /* Gradients of vdn_sink_attn from its inputs, its o and lse, and d_o =
  * dLoss/do.  Deterministic: the same call gives the same bits.
  * o, d_o   : [Lq, ld] bf16;  lse: fp32 [H, Lq] (of the forward call)
  * dq       : [Lq, ld_dq] bf16;  dk, dv: [Lk, ld_dkv] bf16; none may overlap
- *            an input.  Rows of no sequence are not written; keys that no
- *            query sees and queries that see nothing get zeros.
+ *            an input.  Keys that no query sees and queries that see nothing
+ *            get zeros.
+ * zero_rest: bits 0, 1, 2: zero the rows of dq, dk, dv of no sequence; where
+ *            the bit is clear they stay as they are
  * ws       : >= vdn_sink_attn_backward_workspace(shape) bytes
  * P and dS are rounded to bf16 for their products; sums in fp32. */
 VDN_API size_t vdn_sink_attn_backward_workspace(const vdn_sink_shape* shape);
@@ -539,8 +544,8 @@ VDN_API vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const voi
                                           const int32_t* cu_k, float scale, const void* o,
                                           int64_t ld_o, const float* lse, const void* d_o,
                                           int64_t ld_do, void* dq, int64_t ld_dq, void* dk,
-                                          void* dv, int64_t ld_dkv, void* ws, size_t ws_bytes,
-                                          void* stream);
+                                          void* dv, int64_t ld_dkv, unsigned zero_rest, void* ws,
+                                          size_t ws_bytes, void* stream);
 
 /* One new token per sequence of a causal stream with a sliding window and
  * sinks: vdn_sink_attn with ahead = 0 for the last query of each sequence, over

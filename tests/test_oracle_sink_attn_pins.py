@@ -101,7 +101,7 @@ def test_bad_shapes_are_refused_on_the_host(L, change, code):
     lib, P = L.lib(), ctypes.c_void_p
     s = _shape(L, **change)
     assert lib.vdn_sink_attn(ctypes.byref(s), P(A), 512, P(A), P(A), 256, None, None, 0.0, P(A),
-                             512, None, P(A), 1 << 40, None) == code
+                             512, 0, None, P(A), 1 << 40, None) == code
     if change != dict(B=2):
         assert lib.vdn_sink_attn_workspace(ctypes.byref(s)) == 0
 
@@ -117,7 +117,7 @@ def test_bad_arguments_are_refused_on_the_host(L, change):
     s = _shape(L)
     assert lib.vdn_sink_attn(ctypes.byref(s), P(a["q"]), a["ld_q"], P(a["k"]), P(a["v"]),
                              a["ld_kv"], P(a["cu_q"]), None, 0.0, P(a["o"]), a["ld_o"],
-                             P(a["lse"]), P(A), 1 << 40, None) == 1
+                             0, P(a["lse"]), P(A), 1 << 40, None) == 1
 
 
 def test_workspaces(L):
@@ -129,11 +129,11 @@ def test_workspaces(L):
     assert n > 256 + 2 * 16 * 4 * 128 * 4
     for ws, size in ((0, 1 << 40), (A + 128, 1 << 40), (A, n - 1)):
         assert lib.vdn_sink_attn(ctypes.byref(few), P(A), 512, P(A), P(A), 256, None, None, 0.0,
-                                 P(A), 512, None, P(ws), size, None) == 3
+                                 P(A), 512, 0, None, P(ws), size, None) == 3
     # no queries: nothing to do, nothing enqueued
     none = _shape(L, Lq=0)
     assert lib.vdn_sink_attn(ctypes.byref(none), None, 512, P(A), P(A), 256, None, None, 0.0,
-                             None, 512, None, P(A), 256, None) == 0
+                             None, 512, 0, None, P(A), 256, None) == 0
 
 
 @pytest.mark.parametrize("change,code", [
@@ -149,7 +149,7 @@ def test_bad_gradient_arguments_are_refused_on_the_host(L, change, code):
     assert lib.vdn_sink_attn_backward(
         ctypes.byref(s), P(a["q"]), 512, P(A), P(A), 256, None, None, 0.0, P(a["o"]), 512,
         P(a["lse"]), P(a["d_o"]), 512, P(a["dq"]), a["ld_dq"], P(a["dk"]), P(a["dv"]),
-        a["ld_dkv"], P(a["ws"]), a["ws_bytes"], None) == code
+        a["ld_dkv"], 0, P(a["ws"]), a["ws_bytes"], None) == code
 
 
 @pytest.mark.parametrize("change,code", BAD_SHAPES)
@@ -158,7 +158,7 @@ def test_bad_gradient_shapes_are_refused_on_the_host(L, change, code):
     s = _shape(L, **change)
     assert lib.vdn_sink_attn_backward(
         ctypes.byref(s), P(A), 512, P(A), P(A), 256, None, None, 0.0, P(A), 512, P(A), P(A), 512,
-        P(A), 512, P(A), P(A), 256, P(A), 1 << 40, None) == code
+        P(A), 512, P(A), P(A), 256, 0, P(A), 1 << 40, None) == code
 
 
 @pytest.mark.parametrize("change,code", [

@@ -180,6 +180,10 @@ def test_other_sequences_and_rows_of_none_do_not_reach_in(vdn):
             assert torch.equal(out[n][20:120], clean[0][n])
             assert torch.equal(out[n][250:320], clean[1][n])
             assert (out[n][:20] == 9).all() and (out[n][320:] == 9).all()
+        fresh = vdn.sink_attn_backward(q, k, v, o, lse, g, H, H, d, **mask)
+        for n in range(3):                              # zeros in a new output
+            assert torch.equal(fresh[n][20:120], clean[0][n])
+            assert not fresh[n][:20].any() and not fresh[n][320:].any()
 
 
 def test_keys_no_query_sees_and_no_queries_at_all(vdn):

@@ -144,6 +144,15 @@ def test_other_sequences_and_rows_of_none_do_not_reach_in(vdn):
         assert torch.equal(out[20:120], clean[0]) and torch.equal(out[250:320], clean[1])
         for none in (slice(0, 20), slice(320, 400)):
             assert (out[none] == 9).all() and (lse[:, none] == 9).all()
+        fresh = vdn.sink_attn(q, k, v, H, H, d, 50, 4, cu_q=cu, cu_k=cu)[0]
+        assert torch.equal(fresh[20:120], clean[0]) and torch.equal(fresh[250:320], clean[1])
+        assert not fresh[:20].any() and not fresh[320:].any()   # zeros in a new output
+    few = torch.tensor([5, 9], dtype=torch.int32, device="cuda")    # split over the keys
+    kv = torch.tensor([0, 4000], dtype=torch.int32, device="cuda")
+    q, k, v, _, _ = make([12], [4000], H, H, d)
+    fresh = vdn.sink_attn(q, k, v, H, H, d, None, cu_q=few, cu_k=kv)[0]
+    assert torch.equal(fresh[5:9], vdn.sink_attn(q[5:9], k, v, H, H, d, None)[0])
+    assert not fresh[:5].any() and not fresh[9:].any()
 
 
 def test_boundaries_outside_the_rows_are_clamped(vdn):

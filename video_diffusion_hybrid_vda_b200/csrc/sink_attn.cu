@@ -46,6 +46,7 @@ struct SinkOut {
   float* lse;        // [H, Lq] or null
   float* part_o;     // [splits, Lq, H, DH]
   float* part_lse;   // [splits, H, Lq]
+  bool zero_rest;    // zero the rows of o of no sequence
 };
 
 // Softmax of one 128-query tile: one thread per query.
@@ -87,6 +88,15 @@ __device__ __forceinline__ void sink_softmax(int i, uint32_t tmem, uint64_t* s_f
     const int c_end = min(valid, p + m.ahead + 1 - ks);  // visible columns: below this, and
     const int c_win = p - m.window + 1 - ks;             // from this on
     const int c_sink = m.sinks - ks;                     // or below this
+    auto hide = [&](int c0) {  // of columns [c0, c0 + 64), those that are not visible
+#pragma unroll
+      for (int w = c0; w < c0 + 64; w += 32) {
+        const uint32_t see = sink_bits(c_win - w, c_end - w, c_sink - w);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          sr[w + c] = see & (1u << c) ? sr[w + c] : __float_as_uint(-INFINITY);
+      }
+    };
     tmem_ld32(s_addr, s0);
     tmem_ld32(s_addr + 32, s1);
     tmem_ld_wait();
@@ -94,11 +104,7 @@ __device__ __forceinline__ void sink_softmax(int i, uint32_t tmem, uint64_t* s_f
     reg_fence(s1);
     tmem_ld32(s_addr + 64, s2);
     tmem_ld32(s_addr + 96, s3);
-    if (edge) {
-#pragma unroll
-      for (int c = 0; c < 64; ++c)
-        if (c >= c_end || (c < c_win && c >= c_sink)) sr[c] = __float_as_uint(-INFINITY);
-    }
+    if (edge) hide(0);
     auto sv = [&](int c) { return __uint_as_float(sr[c]); };
     float mx8[8];
 #pragma unroll
@@ -112,11 +118,7 @@ __device__ __forceinline__ void sink_softmax(int i, uint32_t tmem, uint64_t* s_f
     tmem_ld_wait();
     reg_fence(s2);
     reg_fence(s3);
-    if (edge) {
-#pragma unroll
-      for (int c = 64; c < 128; ++c)
-        if (c >= c_end || (c < c_win && c >= c_sink)) sr[c] = __float_as_uint(-INFINITY);
-    }
+    if (edge) hide(64);
 #pragma unroll
     for (int c = 64; c < 128; c += 16)
 #pragma unroll
@@ -260,6 +262,8 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
   // Heaviest first: the last queries of a sequence see the most keys.
   const int slots = sink_slots(dims.Lq, dims.B, 256);
   const int per_slot = dims.H * splits;
+  if (out.zero_rest && out.o != nullptr)
+    sink_zero_rest(dims.cu_q, dims.B, dims.Lq, out.o, out.ld_o, dims.H * DH);
   const int slot = slots - 1 - static_cast<int>(blockIdx.x) / per_slot;
   const int h = static_cast<int>(blockIdx.x) % per_slot / splits;
   const int split = static_cast<int>(blockIdx.x) % splits;
@@ -457,7 +461,8 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
   }
 }
 
-// o and lse of (row, head) from its parts: a warp each, DH / 32 columns a lane.
+// o and lse of (row, head) from its parts: a warp each, DH / 32 columns a
+// lane; lane s holds part s's lse (at most 32 parts).
 template <int DH>
 __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, int splits,
                                                            const SinkOut parts,
@@ -465,32 +470,39 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
                                                            int64_t ld_o,
                                                            float* __restrict__ lse) {
   constexpr int W = DH / 32;
+  if (parts.zero_rest) sink_zero_rest(dims.cu_q, dims.B, dims.Lq, o, ld_o, dims.H * DH);
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
   const int r = static_cast<int>(w / dims.H), h = static_cast<int>(w % dims.H);
   if (r >= dims.Lq) return;
-  if (dims.cu_q != nullptr &&  // rows of no sequence have no parts and stay as they are
+  if (dims.cu_q != nullptr &&  // rows of no sequence have no parts
       (r < sink_bound(dims.cu_q, 0, dims.Lq) || r >= sink_bound(dims.cu_q, dims.B, dims.Lq)))
     return;
-  const int64_t at = static_cast<int64_t>(h) * dims.Lq + r, step = static_cast<int64_t>(dims.H) *
-                                                                   dims.Lq;
-  float top = -INFINITY;
-  for (int s = 0; s < splits; ++s) top = fmaxf(top, parts.part_lse[s * step + at]);
-  float sum = 0.f, acc[W] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float part = parts.part_lse[s * step + at];
-    if (part == -INFINITY) continue;  // saw nothing (a NaN goes through)
-    const float f = __expf(part - top);
-    sum += f;
-    const float* src = parts.part_o + ((static_cast<int64_t>(s) * dims.Lq + r) * dims.H + h) * DH;
+  const int lane = lane_id();
+  const int64_t at = static_cast<int64_t>(h) * dims.Lq + r;
+  const int64_t step = static_cast<int64_t>(dims.H) * dims.Lq;
+  const float part = lane < splits ? parts.part_lse[lane * step + at] : -INFINITY;
+  float top = part;
 #pragma unroll
-    for (int c = 0; c < W; ++c) acc[c] += f * src[32 * c + lane_id()];
+  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+  // a part that saw nothing weighs 0 (its fp32 rows are zeros); a NaN goes through
+  const float f = part == -INFINITY ? 0.f : __expf(part - top);
+  float sum = f;
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  float acc[W] = {};
+  const float* src = parts.part_o + (static_cast<int64_t>(r) * dims.H + h) * DH + lane;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    const float fs = __shfl_sync(0xffffffffu, f, s);
+#pragma unroll
+    for (int c = 0; c < W; ++c) acc[c] += fs * src[32 * c];
+    src += step * DH;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
   for (int c = 0; c < W; ++c)
-    o[static_cast<int64_t>(r) * ld_o + h * DH + 32 * c + lane_id()] = __float2bfloat16(acc[c] *
-                                                                                       inv);
-  if (lse != nullptr && lane_id() == 0) lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
+    o[static_cast<int64_t>(r) * ld_o + h * DH + 32 * c + lane] = __float2bfloat16(acc[c] * inv);
+  if (lse != nullptr && lane == 0) lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 // Splits of each CTA's key tiles: only where the CTAs would leave most of 148
@@ -513,7 +525,8 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 template <int DH>
 cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, int splits,
                         const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
-                        float scale, __nv_bfloat16* o, int64_t ld_o, float* lse, uint8_t* ws) {
+                        float scale, __nv_bfloat16* o, int64_t ld_o, float* lse, bool zero_rest,
+                        uint8_t* ws) {
   using Cfg = SinkCfg<DH>;
   static std::atomic<uint64_t> smem_set{0};
   if (cudaError_t e = set_smem_once(sink_attn_kernel<DH>, Cfg::SMEM, smem_set)) return e;
@@ -521,6 +534,7 @@ cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, int splits,
   out.o = splits == 1 ? o : nullptr;
   out.ld_o = ld_o;
   out.lse = lse;
+  out.zero_rest = zero_rest && dims.cu_q != nullptr;
   out.part_o = reinterpret_cast<float*>(ws + kStatusBytes);
   out.part_lse = reinterpret_cast<float*>(
       ws + kStatusBytes +
@@ -590,8 +604,8 @@ size_t vdn_sink_attn_workspace(const vdn_sink_shape* shape) {
 
 vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_q, const void* k,
                          const void* v, int64_t ld_kv, const int32_t* cu_q, const int32_t* cu_k,
-                         float scale, void* o, int64_t ld_o, float* lse_opt, void* ws,
-                         size_t ws_bytes, void* stream) {
+                         float scale, void* o, int64_t ld_o, int zero_rest, float* lse_opt,
+                         void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx("vdn_sink_attn");
   vdn_sink_shape s;
   const vdn_status r = sink_check(shape, q, ld_q, k, v, ld_kv, cu_q, cu_k, &s);
@@ -620,9 +634,11 @@ vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_
   const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
   auto* ob = static_cast<__nv_bfloat16*>(o);
   auto* wb = static_cast<uint8_t*>(ws);
+  const bool z = zero_rest != 0;
   const cudaError_t e =
-      s.d == 128 ? launch_sink<128>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, wb)
-                 : launch_sink<64>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, wb);
+      s.d == 128
+          ? launch_sink<128>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, z, wb)
+          : launch_sink<64>(ctx, dims, splits, qmap, kmap, vmap, sc, ob, ld_o, lse_opt, z, wb);
   return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
 }
 

@@ -117,6 +117,30 @@ __device__ __forceinline__ bool sink_sees_all(const SinkMask& m, int pa, int pb,
   return ke <= pa + m.ahead && (ks > pb - m.window || ke < m.sinks);
 }
 
+// Visibility of 32 consecutive columns as bits: the columns [lo, hi) and those
+// below `sink` (bounds relative to the first of the 32).  A tile that crosses
+// the mask's edge then pays one bit test and one select an element.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+__device__ __forceinline__ uint32_t sink_bits(int lo, int hi, int sink) {
+  return bits_below(hi) & (~bits_below(lo) | bits_below(sink));
+}
+
+// Rows of no sequence: before the first boundary and from the last one on.
+// Zeroed by all threads of the grid together (row r by block r mod grid).
+__device__ __forceinline__ void sink_zero_rest(const int32_t* cu, int B, int L, void* base,
+                                               int64_t ld, int cols) {
+  const int head = sink_bound(cu, 0, L), tail = max(head, sink_bound(cu, B, L));
+  const int rest = head + L - tail;
+  for (int64_t i = blockIdx.x; i < rest; i += gridDim.x) {
+    const int64_t r = i < head ? i : tail + (i - head);
+    uint4* row = reinterpret_cast<uint4*>(static_cast<uint8_t*>(base) + r * ld * 2);
+    for (int c = threadIdx.x; c < cols / 8; c += blockDim.x) row[c] = make_uint4(0, 0, 0, 0);
+  }
+}
+
 // Zero rows [from, 128) of a tile of `slabs` 64-column slabs (128 rows x 128
 // swizzled bytes each): the whole warp.  Zeroing whole rows needs no swizzle.
 // The rows belong to another sequence or lie past the last one; as the

@@ -46,45 +46,77 @@ struct GradCfg {
 
 // Per query, in tiles of 128 (the slots of sink_attn.cuh): -lse log2 e and
 // D = dO . o.  Rows past the sequence's end get -inf and 0: P = 0 there.
-__global__ void __launch_bounds__(256) sink_stats_kernel(
-    const SinkDims dims, int DH, const __nv_bfloat16* __restrict__ o, int64_t ld_o,
-    const __nv_bfloat16* __restrict__ d_o, int64_t ld_do, const float* __restrict__ lse,
-    float* __restrict__ nlse2, float* __restrict__ delta) {
-  // a block: 32 rows of a slot, all heads; DH / 8 lanes a (row, head)
-  const int slot = blockIdx.x >> 2;
+// Rows of dq, dk and dv of no sequence are zeroed where asked.
+// A block takes 8 rows of a slot, DH / 8 lanes a (row, head), four at a time
+// in flight: reading o and dO once is the whole cost.
+struct StatsArgs {
+  int DH;
+  const __nv_bfloat16* o;
+  const __nv_bfloat16* d_o;
+  int64_t ld_o, ld_do;
+  const float* lse;
+  float* nlse2;
+  float* delta;
+  void* zero[3];       // dq, dk, dv or null
+  int64_t ld_zero[3];
+};
+
+constexpr int kStatsRows = 8;
+
+__global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, const StatsArgs a) {
+  constexpr int U = 4;
+  if (dims.cu_q != nullptr) {
+    if (a.zero[0] != nullptr)
+      sink_zero_rest(dims.cu_q, dims.B, dims.Lq, a.zero[0], a.ld_zero[0], dims.H * a.DH);
+    for (int i = 1; i < 3; ++i)
+      if (a.zero[i] != nullptr)
+        sink_zero_rest(dims.cu_k, dims.B, dims.Lk, a.zero[i], a.ld_zero[i], dims.Hkv * a.DH);
+  }
+  const int slot = blockIdx.x / (128 / kStatsRows);
   const int slots = sink_slots(dims.Lq, dims.B, 128);
+  if (slot >= slots) return;
   const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
   const SinkSeq seq = sink_seq(dims, b);
   const int tile0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
   if (tile0 >= seq.q1) return;
-  const int first = (blockIdx.x & 3) * 32;
-  const int lanes = DH / 8, step = 256 / lanes;
-  const int lane = threadIdx.x % lanes;
-  // rows innermost in the slot order of a warp's lanes would scatter the
-  // loads; heads innermost read whole rows
-  for (int base = 0; base < 32 * dims.H; base += step) {
-    const int s = base + threadIdx.x / lanes;
-    const int i = s / dims.H, h = s - i * dims.H;
-    const int r = tile0 + first + i;
-    float t = 0.f;
-    const bool on = i < 32 && r < seq.q1;
-    if (on) {
-      const uint4 x = *reinterpret_cast<const uint4*>(o + r * ld_o + h * DH + 8 * lane);
-      const uint4 y = *reinterpret_cast<const uint4*>(d_o + r * ld_do + h * DH + 8 * lane);
-      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  const int first = blockIdx.x % (128 / kStatsRows) * kStatsRows;
+  const int lanes = a.DH / 8, step = 256 / lanes;
+  const int lane = threadIdx.x % lanes, total = kStatsRows * dims.H;
+  for (int base = threadIdx.x / lanes; base - static_cast<int>(threadIdx.x / lanes) < total;
+       base += U * step) {
+    uint4 x[U], y[U];
+    bool on[U];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = unpack_bf16x2(xs[e]), c = unpack_bf16x2(ys[e]);
-        t += a.x * c.x + a.y * c.y;
+    for (int n = 0; n < U; ++n) {
+      const int s = base + n * step, i = s / dims.H, h = s - i * dims.H;
+      const int64_t r = tile0 + first + i;
+      on[n] = s < total && r < seq.q1;
+      x[n] = y[n] = make_uint4(0, 0, 0, 0);
+      if (on[n]) {
+        x[n] = *reinterpret_cast<const uint4*>(a.o + r * a.ld_o + h * a.DH + 8 * lane);
+        y[n] = *reinterpret_cast<const uint4*>(a.d_o + r * a.ld_do + h * a.DH + 8 * lane);
       }
     }
-    for (int w = lanes >> 1; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
-    if (lane == 0 && i < 32) {
-      const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + first + i;
-      const float v = on ? lse[static_cast<int64_t>(h) * dims.Lq + r] : -INFINITY;
-      const bool none = v == -INFINITY;
-      nlse2[at] = none ? -INFINITY : -v * 1.4426950408889634f;
-      delta[at] = none ? 0.f : t;
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const uint32_t xs[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      const uint32_t ys[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
+      float t = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack_bf16x2(xs[e]), g = unpack_bf16x2(ys[e]);
+        t += f.x * g.x + f.y * g.y;
+      }
+      for (int w = lanes >> 1; w > 0; w >>= 1) t += __shfl_xor_sync(0xffffffffu, t, w);
+      const int s = base + n * step, i = s / dims.H, h = s - i * dims.H;
+      if (lane == 0 && s < total) {
+        const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + first + i;
+        const float v =
+            on[n] ? a.lse[static_cast<int64_t>(h) * dims.Lq + tile0 + first + i] : -INFINITY;
+        const bool none = v == -INFINITY;
+        a.nlse2[at] = none ? -INFINITY : -v * 1.4426950408889634f;
+        a.delta[at] = none ? 0.f : t;
+      }
     }
   }
 }
@@ -163,6 +195,7 @@ __device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t*
     const bool edge = !sink_sees_all(m, p0, p0 + 63, kw, kw + 31);
     const int c_lo = key - m.ahead - p0;                     // visible columns [c_lo, c_hi)
     const int c_hi = key < m.sinks ? 64 : key - p0 + m.window;
+    const uint32_t see[2] = {sink_bits(c_lo, c_hi, 0), sink_bits(c_lo - 32, c_hi - 32, 0)};
     if (!__all_sync(0xffffffffu, mbar_wait(&st_full[s], (t / Cfg::STAGES) & 1, budget_ns) &&
                                      mbar_wait(s_full, t & 1, budget_ns)))
       return false;
@@ -191,8 +224,7 @@ __device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t*
     }
     if (edge) {
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
-        if (c < c_lo || c >= c_hi) x[c] = 0;
+      for (int c = 0; c < 64; ++c) x[c] = see[c >> 5] & (1u << (c & 31)) ? x[c] : 0;
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -216,6 +248,10 @@ __device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t*
       tmem_ld32(dp_addr + 32 * q, g);
       tmem_ld_wait();
       reg_fence(g);
+      if (edge) {  // dP of a hidden pair may be NaN, and 0 x NaN is not 0
+#pragma unroll
+        for (int c = 0; c < 32; ++c) g[c] = see[q] & (1u << c) ? g[c] : 0;
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const ulonglong2 d2 = dl[8 * q + e];
@@ -223,12 +259,9 @@ __device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t*
         for (int f = 0; f < 2; ++f) {
           const uint64_t d = f ? d2.y : d2.x;
           const int c = 4 * e + 2 * f;
-          float a = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - f32x2_lo(d));
-          float b = __uint_as_float(x[32 * q + c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d));
-          if (edge) {  // 0 x NaN of a hidden pair
-            if (32 * q + c < c_lo || 32 * q + c >= c_hi) a = 0.f;
-            if (32 * q + c + 1 < c_lo || 32 * q + c + 1 >= c_hi) b = 0.f;
-          }
+          const float a = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - f32x2_lo(d));
+          const float b =
+              __uint_as_float(x[32 * q + c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d));
           ds[16 * q + 2 * e + f] = pack_bf16x2(a, b);
         }
       }
@@ -737,6 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool edge = valid < 64 || !sink_sees_all(m, pw, pw + 31, ks, ks + 63);
       const int c_end = min(valid, p + m.ahead + 1 - ks);
       const int c_win = p - m.window + 1 - ks, c_sink = m.sinks - ks;
+      const uint32_t see[2] = {sink_bits(c_win, c_end, c_sink),
+                               sink_bits(c_win - 32, c_end - 32, c_sink - 32)};
       if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, budget_ns))) {
         ok = false;
         break;
@@ -769,11 +804,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         reg_fence(g);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float v = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - dl);
-          if (edge && (32 * q + c >= c_end || (32 * q + c < c_win && 32 * q + c >= c_sink)))
-            v = 0.f;
-          g[c] = __float_as_uint(v);
+        for (int c = 0; c < 32; ++c)
+          g[c] = __float_as_uint(__uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - dl));
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) g[c] = see[q] & (1u << c) ? g[c] : 0;
         }
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -879,21 +914,16 @@ struct GradMaps {
 
 template <int DH>
 cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const GradMaps& t,
-                             const FarPlan& far, KeyPass a, const __nv_bfloat16* o, int64_t ld_o,
-                             const __nv_bfloat16* d_o, int64_t ld_do, const float* lse,
-                             float* nlse2, float* delta, float scale, __nv_bfloat16* dq,
-                             int64_t ld_dq) {
+                             const FarPlan& far, const KeyPass& a, const StatsArgs& st,
+                             float scale, __nv_bfloat16* dq, int64_t ld_dq) {
   using Cfg = GradCfg<DH>;
   static std::atomic<uint64_t> set_near{0}, set_far{0}, set_query{0};
   if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, false>, Cfg::SMEM, set_near)) return e;
   if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, true>, Cfg::SMEM, set_far)) return e;
   if (cudaError_t e = set_smem_once(sink_query_pass_kernel<DH>, Cfg::SMEM, set_query)) return e;
   const int q_slots = sink_slots(dims.Lq, dims.B, 128);
-  if (dims.Lq > 0) {
-    sink_stats_kernel<<<4 * q_slots, 256, 0, ctx.stream>>>(dims, DH, o, ld_o, d_o, ld_do, lse,
-                                                           nlse2, delta);
-    if (cudaError_t e = cudaGetLastError()) return e;
-  }
+  sink_stats_kernel<<<128 / kStatsRows * q_slots, 256, 0, ctx.stream>>>(dims, st);
+  if (cudaError_t e = cudaGetLastError()) return e;
   if (far.parts > 0) {
     sink_key_pass_kernel<DH, true>
         <<<dims.B * far.tiles * dims.Hkv * far.parts, kThreads, Cfg::SMEM, ctx.stream>>>(
@@ -908,7 +938,7 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
   }
   if (dims.Lq > 0)
     sink_query_pass_kernel<DH><<<q_slots * dims.H, kThreads, Cfg::SMEM, ctx.stream>>>(
-        t.q, t.d_o, t.k, t.v, dims, nlse2, delta, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
+        t.q, t.d_o, t.k, t.v, dims, a.nlse2, a.delta, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
   return cudaGetLastError();
 }
 
@@ -935,7 +965,8 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
                                   const int32_t* cu_q, const int32_t* cu_k, float scale,
                                   const void* o, int64_t ld_o, const float* lse, const void* d_o,
                                   int64_t ld_do, void* dq, int64_t ld_dq, void* dk, void* dv,
-                                  int64_t ld_dkv, void* ws, size_t ws_bytes, void* stream) {
+                                  int64_t ld_dkv, unsigned zero_rest, void* ws, size_t ws_bytes,
+                                  void* stream) {
   NvtxRange nvtx("vdn_sink_attn_backward");
   vdn_sink_shape s;
   const vdn_status r = sink_check(shape, q, ld_q, k, v, ld_kv, cu_q, cu_k, &s);
@@ -983,11 +1014,21 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
   const Launch ctx{static_cast<cudaStream_t>(stream), static_cast<uint32_t*>(ws),
                    current_wait_budget_ns()};
   const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
+  StatsArgs st{};
+  st.DH = s.d;
+  st.o = static_cast<const __nv_bfloat16*>(o);
+  st.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  st.ld_o = ld_o, st.ld_do = ld_do;
+  st.lse = lse, st.nlse2 = nlse2, st.delta = delta;
+  void* outs[3] = {dq, dk, dv};
+  const int64_t lds[3] = {ld_dq, ld_dkv, ld_dkv};
+  for (int i = 0; i < 3; ++i) {
+    st.zero[i] = zero_rest >> i & 1u ? outs[i] : nullptr;
+    st.ld_zero[i] = lds[i];
+  }
   auto run = [&](auto dh) {
-    return launch_sink_grad<decltype(dh)::value>(
-        ctx, dims, t, lay.far, a, static_cast<const __nv_bfloat16*>(o), ld_o,
-        static_cast<const __nv_bfloat16*>(d_o), ld_do, lse, nlse2, delta, sc,
-        static_cast<__nv_bfloat16*>(dq), ld_dq);
+    return launch_sink_grad<decltype(dh)::value>(ctx, dims, t, lay.far, a, st, sc,
+                                                 static_cast<__nv_bfloat16*>(dq), ld_dq);
   };
   const cudaError_t e = s.d == 128 ? run(std::integral_constant<int, 128>{})
                                    : run(std::integral_constant<int, 64>{});

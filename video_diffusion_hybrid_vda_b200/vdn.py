@@ -174,13 +174,14 @@ def lib():
     K = ctypes.POINTER(SinkShape)
     L.vdn_sink_attn_workspace.argtypes = [K]
     L.vdn_sink_attn_workspace.restype = _SZ
-    L.vdn_sink_attn.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P, _I64, _P,
-                                _P, _SZ, _P]
+    L.vdn_sink_attn.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P, _I64,
+                                ctypes.c_int, _P, _P, _SZ, _P]
     L.vdn_sink_attn.restype = ctypes.c_int
     L.vdn_sink_attn_backward_workspace.argtypes = [K]
     L.vdn_sink_attn_backward_workspace.restype = _SZ
     L.vdn_sink_attn_backward.argtypes = [K, _P, _I64, _P, _P, _I64, _P, _P, ctypes.c_float, _P,
-                                         _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64, _P, _SZ, _P]
+                                         _I64, _P, _P, _I64, _P, _I64, _P, _P, _I64,
+                                         ctypes.c_uint, _P, _SZ, _P]
     L.vdn_sink_attn_backward.restype = ctypes.c_int
     L.vdn_sink_attn_step.argtypes = [ctypes.c_int] * 6 + [_P, _I64, _P, _P, _I64, _P, _P, _I64,
                                                           _I64, _P, ctypes.c_float, _P, _I64, _P]
@@ -619,27 +620,61 @@ NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
 
 
 def _same_device(*ts):
-    """Every tensor on the current CUDA device (the kernels are launched there)."""
-    _need_cuda(*ts)
+    """Every tensor on the current CUDA device (the kernels are launched
+    there); returns its index."""
     cur = torch.cuda.current_device()
     for t in ts:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
+            _need_cuda(t)
             raise ValueError(f"libvdn: tensor on {t.device}, but the current device is cuda:{cur}")
+    return cur
 
 
-def _rows2d(name, t, cols, dtype, rows=None):
-    """t must be a [rows, >= cols] matrix with unit column stride and the dtype."""
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{rows or 'rows'}, {cols}]")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.shape[0] and t.shape[1] and t.stride(1) != 1:
+# The raw handle of the current stream without building a Stream object (the
+# calls below are short enough for its cost to show), where torch offers it.
+_raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_current_stream is not None:
+        return _raw_current_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _mat(name, t, rows, cols, dtype):
+    """(address, row stride) of a [rows, cols] matrix of dtype with contiguous
+    columns; one row or none has no stride of its own."""
+    if t.dtype is not dtype or t.shape != (rows, cols):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} [{rows}, {cols}]")
+    if rows <= 1:
+        if rows and cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name}: columns must be contiguous")
+        return t.data_ptr(), cols
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{name}: columns must be contiguous")
+    return t.data_ptr(), ld
 
 
-def _ld(t):
-    """Row stride in elements; one row or none has no stride of its own."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+def _vec(name, t, n):
+    """Address of a contiguous fp32 [n] vector, or None."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous fp32 [{n}]")
+    return t.data_ptr()
+
+
+def _rows_of(name, t):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: a matrix [rows, heads * d]")
+    return t.shape[0]
 
 
 def rope_frequencies(rot, base=10000.0, sections=None, scaling=None, factor=1.0, original=4096,
@@ -720,6 +755,10 @@ class RopePlan:
         words = [self.phase_word(f) for f in self.frequencies]
         signed = [w - (1 << 64) if w >> 63 else w for w in words]
         self.phase = torch.tensor(signed or [0], dtype=torch.int64).to(device or "cuda")
+        pairs = (ctypes.c_int * 4)(*(self.sections + [0] * (4 - len(self.sections))))
+        self._c = RopePlanC(self.d, self.rot, ROPE_LAYOUTS[layout], len(self.sections), pairs,
+                            self.scale, self.phase.data_ptr())
+        self._ref = ctypes.byref(self._c)
 
     @staticmethod
     def phase_word(radians):
@@ -731,22 +770,19 @@ class RopePlan:
     def n_axes(self):
         return len(self.sections)
 
-    def _c(self):
-        pairs = (ctypes.c_int * 4)(*(self.sections + [0] * (4 - len(self.sections))))
-        return RopePlanC(self.d, self.rot, ROPE_LAYOUTS[self.layout], self.n_axes, pairs,
-                         self.scale, self.phase.data_ptr())
-
 
 def _rope_positions(positions, plan, rows):
-    """(pointer, axis stride) of int32 positions [rows] or [axes, rows]."""
+    """(address, axis stride) of int32 positions [rows] or [axes, rows]."""
     if positions is None:
         return None, 0
-    if positions.dtype != torch.int32:
+    if positions.dtype is not torch.int32:
         raise ValueError("positions: int32")
-    p = positions[None] if positions.dim() == 1 else positions
-    if p.dim() != 2 or p.shape != (plan.n_axes, rows) or (rows > 1 and p.stride(1) != 1):
-        raise ValueError(f"positions: [{plan.n_axes}, {rows}] with contiguous rows")
-    return _ptr(p), p.stride(0) if plan.n_axes > 1 else rows
+    n = plan.n_axes
+    if positions.shape != (n, rows) and not (n == 1 and positions.shape == (rows,)):
+        raise ValueError(f"positions: [{n}, {rows}]")
+    if rows > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions: contiguous rows")
+    return positions.data_ptr(), max(positions.stride(0), rows) if n > 1 else rows
 
 
 def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
@@ -754,34 +790,33 @@ def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
     out = R(positions) x, or with ``inverse`` R^T x, which is its gradient.
     positions: int32 [rows] or [axes, rows], default the row index; out may
     be x.  Returns out."""
-    _same_device(x, out, positions, plan.phase)
-    if x.dtype not in DTYPE_CODES:
+    dev = _same_device(x, out, positions, plan.phase)
+    rows, cols, dtype = _rows_of("x", x), H * plan.d, x.dtype
+    code = DTYPE_CODES.get(dtype)
+    if code is None:
         raise ValueError("rope: bf16, fp16 or fp32")
-    _rows2d("x", x, H * plan.d, x.dtype)
-    rows = x.shape[0]
+    xp, ld = _mat("x", x, rows, cols, dtype)
     if out is None:
-        out = torch.empty((rows, H * plan.d), dtype=x.dtype, device=x.device)
-    _rows2d("out", out, H * plan.d, x.dtype, rows)
+        out = torch.empty((rows, cols), dtype=dtype, device=x.device)
+    op, ld_out = _mat("out", out, rows, cols, dtype)
     pos, stride = _rope_positions(positions, plan, rows)
-    c = plan._c()
-    _check(lib().vdn_rope(ctypes.byref(c), DTYPE_CODES[x.dtype], rows, int(H), _ptr(x), _ld(x),
-                          pos, stride, int(bool(inverse)), _ptr(out), _ld(out),
-                          _stream(stream)), "vdn_rope")
+    _check(lib().vdn_rope(plan._ref, code, rows, H, xp, ld, pos, stride, 1 if inverse else 0, op,
+                          ld_out, _raw_stream(stream, dev)), "vdn_rope")
     return out
 
 
-def _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions):
-    if q.dtype not in DTYPE_CODES:
+def _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions):
+    """The arguments qk_norm_rope and its gradients share, in the C order."""
+    rows = _rows_of("q", q)
+    code = DTYPE_CODES.get(q.dtype)
+    if code is None:
         raise ValueError("qk_norm_rope: bf16, fp16 or fp32")
     if q_norm not in NORMS or k_norm not in NORMS:
         raise ValueError("norm: 'rms', 'l2' or 'none'")
-    _rows2d("q", q, H * plan.d, q.dtype)
-    _rows2d("k", k, H_kv * plan.d, q.dtype, q.shape[0])
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (plan.d,) or
-                              not w.is_contiguous()):
-            raise ValueError(f"{name}: contiguous fp32 [{plan.d}]")
-    return _rope_positions(positions, plan, q.shape[0])
+    return (plan._ref, code, rows, H, H_kv, *_mat("q", q, rows, H * plan.d, q.dtype),
+            *_mat("k", k, rows, H_kv * plan.d, q.dtype), NORMS[q_norm], NORMS[k_norm],
+            _vec("wq", wq, plan.d), _vec("wk", wk, plan.d), eps,
+            *_rope_positions(positions, plan, rows))
 
 
 def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rms", eps=1e-6,
@@ -790,20 +825,17 @@ def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rm
     in one pass.  Norms: "rms", "l2" (unit length, as vda_scan takes keys) or
     "none"; wq, wk: fp32 [d] or None.  Outputs may be the inputs.
     Returns (q_out, k_out)."""
-    _same_device(q, k, wq, wk, positions, q_out, k_out, plan.phase)
-    pos, stride = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions)
-    rows = q.shape[0]
+    dev = _same_device(q, k, wq, wk, positions, q_out, k_out, plan.phase)
+    args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
+    rows, dtype, d = q.shape[0], q.dtype, plan.d
     if q_out is None:
-        q_out = torch.empty((rows, H * plan.d), dtype=q.dtype, device=q.device)
+        q_out = torch.empty((rows, H * d), dtype=dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty((rows, H_kv * plan.d), dtype=q.dtype, device=q.device)
-    _rows2d("q_out", q_out, H * plan.d, q.dtype, rows)
-    _rows2d("k_out", k_out, H_kv * plan.d, q.dtype, rows)
-    c = plan._c()
+        k_out = torch.empty((rows, H_kv * d), dtype=dtype, device=q.device)
     _check(lib().vdn_qk_norm_rope(
-        ctypes.byref(c), DTYPE_CODES[q.dtype], rows, int(H), int(H_kv), _ptr(q), _ld(q), _ptr(k),
-        _ld(k), NORMS[q_norm], NORMS[k_norm], _ptr(wq), _ptr(wk), float(eps), pos, stride,
-        _ptr(q_out), _ld(q_out), _ptr(k_out), _ld(k_out), _stream(stream)), "vdn_qk_norm_rope")
+        *args, *_mat("q_out", q_out, rows, H * d, dtype),
+        *_mat("k_out", k_out, rows, H_kv * d, dtype), _raw_stream(stream, dev)),
+        "vdn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -813,33 +845,24 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
     """Gradients of qk_norm_rope from its inputs and its outputs' gradients.
     Returns (dq, dk, dwq, dwk, ws): dwq and dwk fp32 [d], None where the side
     has no norm.  dq may be dq_out and dk dk_out."""
-    _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
-    pos, stride = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, positions)
-    rows, dev = q.shape[0], q.device
+    dev = _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
+    args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
+    rows, dtype, d, device = q.shape[0], q.dtype, plan.d, q.device
     if dq is None:
-        dq = torch.empty((rows, H * plan.d), dtype=q.dtype, device=dev)
+        dq = torch.empty((rows, H * d), dtype=dtype, device=device)
     if dk is None:
-        dk = torch.empty((rows, H_kv * plan.d), dtype=q.dtype, device=dev)
-    for name, t, h in (("dq_out", dq_out, H), ("dk_out", dk_out, H_kv), ("dq", dq, H),
-                       ("dk", dk, H_kv)):
-        _rows2d(name, t, h * plan.d, q.dtype, rows)
+        dk = torch.empty((rows, H_kv * d), dtype=dtype, device=device)
     if dwq is None and NORMS[q_norm]:
-        dwq = torch.empty(plan.d, dtype=torch.float32, device=dev)
+        dwq = torch.empty(d, dtype=torch.float32, device=device)
     if dwk is None and NORMS[k_norm]:
-        dwk = torch.empty(plan.d, dtype=torch.float32, device=dev)
-    for name, w in (("dwq", dwq), ("dwk", dwk)):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (plan.d,) or
-                              not w.is_contiguous()):
-            raise ValueError(f"{name}: contiguous fp32 [{plan.d}]")
+        dwk = torch.empty(d, dtype=torch.float32, device=device)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(plan.d)), dev)
-    c = plan._c()
+        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), device)
     _check(lib().vdn_qk_norm_rope_backward(
-        ctypes.byref(c), DTYPE_CODES[q.dtype], rows, int(H), int(H_kv), _ptr(q), _ld(q), _ptr(k),
-        _ld(k), NORMS[q_norm], NORMS[k_norm], _ptr(wq), _ptr(wk), float(eps), pos, stride,
-        _ptr(dq_out), _ld(dq_out), _ptr(dk_out), _ld(dk_out), _ptr(dq), _ld(dq), _ptr(dk),
-        _ld(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), ws.numel(), _stream(stream)),
-        "vdn_qk_norm_rope_backward")
+        *args, *_mat("dq_out", dq_out, rows, H * d, dtype),
+        *_mat("dk_out", dk_out, rows, H_kv * d, dtype), *_mat("dq", dq, rows, H * d, dtype),
+        *_mat("dk", dk, rows, H_kv * d, dtype), _vec("dwq", dwq, d), _vec("dwk", dwk, d),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
 
 
@@ -859,22 +882,31 @@ def sink_attn_workspace(Lq, Lk, B, H, H_kv, d, window, sinks=0, ahead=0):
         ctypes.byref(_sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead))))
 
 
-def _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k):
-    _rows2d("q", q, H * d, torch.bfloat16)
-    _rows2d("k", k, H_kv * d, torch.bfloat16)
-    _rows2d("v", v, H_kv * d, torch.bfloat16, k.shape[0])
-    if _ld(k) != _ld(v):
+def _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale):
+    """(shape, the arguments the forward and the gradient call begin with)."""
+    Lq, Lk, bf16 = _rows_of("q", q), _rows_of("k", k), torch.bfloat16
+    kp, ld_kv = _mat("k", k, Lk, H_kv * d, bf16)
+    vp, ld_v = _mat("v", v, Lk, H_kv * d, bf16)
+    if ld_v != ld_kv:
         raise ValueError("k and v must share one row stride")
     if (cu_q is None) != (cu_k is None):
         raise ValueError("cu_q and cu_k: both or neither")
     B = 1
     if cu_q is not None:
-        if cu_q.dtype != torch.int32 or cu_k.dtype != torch.int32 or cu_q.dim() != 1 or \
-                cu_q.shape != cu_k.shape or cu_q.numel() < 2 or not cu_q.is_contiguous() or \
+        if cu_q.dtype is not torch.int32 or cu_k.dtype is not torch.int32 or cu_q.dim() != 1 or \
+                cu_q.shape != cu_k.shape or cu_q.shape[0] < 2 or not cu_q.is_contiguous() or \
                 not cu_k.is_contiguous():
             raise ValueError("cu_q and cu_k: contiguous int32 [sequences + 1]")
-        B = cu_q.numel() - 1
-    return _sink_shape(q.shape[0], k.shape[0], B, H, H_kv, d, window, sinks, ahead)
+        B = cu_q.shape[0] - 1
+    shape = _sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead)
+    return shape, (ctypes.byref(shape), *_mat("q", q, Lq, H * d, bf16), kp, vp, ld_kv,
+                   _addr(cu_q), _addr(cu_k), scale)
+
+
+def _lse_addr(lse, H, Lq):
+    if lse.dtype is not torch.float32 or lse.shape != (H, Lq) or not lse.is_contiguous():
+        raise ValueError("lse: contiguous fp32 [H, Lq]")
+    return lse.data_ptr()
 
 
 def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=None, scale=0.0,
@@ -884,21 +916,21 @@ def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=Non
     q [Lq, H*d], k and v [Lk, H_kv*d] bf16.  Query at position p sees key j
     iff j <= p + ahead and (p - j < window or j < sinks); the last query of a
     sequence stands at its last key.  window None forgets nothing.  cu_q,
-    cu_k: int32 [B + 1] row offsets of the sequences (None: one sequence).
-    Returns (o, ws); fills ``lse`` [H, Lq] if given."""
-    _same_device(q, k, v, cu_q, cu_k, out, lse, ws)
-    shape = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k)
-    if out is None:
-        out = torch.empty((q.shape[0], H * d), dtype=torch.bfloat16, device=q.device)
-    _rows2d("out", out, H * d, torch.bfloat16, q.shape[0])
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (H, q.shape[0]) or
-                            not lse.is_contiguous()):
-        raise ValueError("lse: contiguous fp32 [H, Lq]")
+    cu_k: int32 [B + 1] row offsets of the sequences (None: one sequence);
+    rows of no sequence are zeros in a new output and stay as they are in
+    ``out`` and ``lse``.  Returns (o, ws); fills ``lse`` [H, Lq] if given."""
+    dev = _same_device(q, k, v, cu_q, cu_k, out, lse, ws)
+    shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
+    Lq = shape.Lq
+    new = out is None
+    if new:
+        out = torch.empty((Lq, H * d), dtype=torch.bfloat16, device=q.device)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(ctypes.byref(shape))), q.device)
-    _check(lib().vdn_sink_attn(ctypes.byref(shape), _ptr(q), _ld(q), _ptr(k), _ptr(v), _ld(k),
-                               _ptr(cu_q), _ptr(cu_k), float(scale), _ptr(out), _ld(out),
-                               _ptr(lse), _ptr(ws), ws.numel(), _stream(stream)), "vdn_sink_attn")
+        ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(args[0])), q.device)
+    _check(lib().vdn_sink_attn(
+        *args, *_mat("out", out, Lq, H * d, torch.bfloat16), 1 if new else 0,
+        None if lse is None else _lse_addr(lse, H, Lq), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, dev)), "vdn_sink_attn")
     return out, ws
 
 
@@ -910,29 +942,28 @@ def sink_attn_backward_workspace(Lq, Lk, B, H, H_kv, d, window, sinks=0, ahead=0
 def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None,
                        cu_k=None, scale=0.0, dq=None, dk=None, dv=None, ws=None, stream=None):
     """Gradients of sink_attn, given its inputs, its o and lse and d_o =
-    dLoss/do.  Returns (dq, dk, dv, ws)."""
-    _same_device(q, k, v, o, lse, d_o, cu_q, cu_k, dq, dk, dv, ws)
-    shape = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k)
-    Lq, Lk, dev = q.shape[0], k.shape[0], q.device
-    if lse.dtype != torch.float32 or lse.shape != (H, Lq) or not lse.is_contiguous():
-        raise ValueError("lse: contiguous fp32 [H, Lq]")
-    # rows of no sequence are not written: they start as zeros
-    new = torch.empty if cu_q is None else torch.zeros
-    dq = new((Lq, H * d), dtype=torch.bfloat16, device=dev) if dq is None else dq
-    dk = new((Lk, H_kv * d), dtype=torch.bfloat16, device=dev) if dk is None else dk
-    dv = new((Lk, H_kv * d), dtype=torch.bfloat16, device=dev) if dv is None else dv
-    for name, t, heads, rows in (("o", o, H, Lq), ("d_o", d_o, H, Lq), ("dq", dq, H, Lq),
-                                 ("dk", dk, H_kv, Lk), ("dv", dv, H_kv, Lk)):
-        _rows2d(name, t, heads * d, torch.bfloat16, rows)
-    if _ld(dk) != _ld(dv):
+    dLoss/do.  Rows of no sequence are zeros in a new output and stay as they
+    are in a given one.  Returns (dq, dk, dv, ws)."""
+    dev = _same_device(q, k, v, o, lse, d_o, cu_q, cu_k, dq, dk, dv, ws)
+    shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
+    Lq, Lk, device, bf16 = shape.Lq, shape.Lk, q.device, torch.bfloat16
+    new = (dq is None) | (dk is None) << 1 | (dv is None) << 2
+    if dq is None:
+        dq = torch.empty((Lq, H * d), dtype=bf16, device=device)
+    if dk is None:
+        dk = torch.empty((Lk, H_kv * d), dtype=bf16, device=device)
+    if dv is None:
+        dv = torch.empty((Lk, H_kv * d), dtype=bf16, device=device)
+    dkp, ld_dkv = _mat("dk", dk, Lk, H_kv * d, bf16)
+    dvp, ld_dv = _mat("dv", dv, Lk, H_kv * d, bf16)
+    if ld_dv != ld_dkv:
         raise ValueError("dk and dv must share one row stride")
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(ctypes.byref(shape))), dev)
+        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), device)
     _check(lib().vdn_sink_attn_backward(
-        ctypes.byref(shape), _ptr(q), _ld(q), _ptr(k), _ptr(v), _ld(k), _ptr(cu_q), _ptr(cu_k),
-        float(scale), _ptr(o), _ld(o), _ptr(lse), _ptr(d_o), _ld(d_o), _ptr(dq), _ld(dq),
-        _ptr(dk), _ptr(dv), _ld(dk), _ptr(ws), ws.numel(), _stream(stream)),
-        "vdn_sink_attn_backward")
+        *args, *_mat("o", o, Lq, H * d, bf16), _lse_addr(lse, H, Lq),
+        *_mat("d_o", d_o, Lq, H * d, bf16), *_mat("dq", dq, Lq, H * d, bf16), dkp, dvp, ld_dkv,
+        new, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_sink_attn_backward")
     return dq, dk, dv, ws
 
 
@@ -945,31 +976,28 @@ def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, win
     in slot p while p < sinks + window, then in slot sinks + (p - sinks) %
     window.  positions: int32 [B], the new tokens' (negative: inactive, its
     cache and row of ``out`` stay as they are).  Returns o [B, H*d]."""
-    _same_device(q, k_new, v_new, k_cache, v_cache, positions, out)
-    B = q.shape[0]
-    _rows2d("q", q, H * d, torch.bfloat16)
-    _rows2d("k_new", k_new, H_kv * d, torch.bfloat16, B)
-    _rows2d("v_new", v_new, H_kv * d, torch.bfloat16, B)
-    if _ld(k_new) != _ld(v_new):
+    dev = _same_device(q, k_new, v_new, k_cache, v_cache, positions, out)
+    B, bf16 = _rows_of("q", q), torch.bfloat16
+    knp, ld_new = _mat("k_new", k_new, B, H_kv * d, bf16)
+    vnp, ld_v = _mat("v_new", v_new, B, H_kv * d, bf16)
+    if ld_v != ld_new:
         raise ValueError("k_new and v_new must share one row stride")
-    shape = (B, int(sinks) + int(window), H_kv * d)
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dtype != torch.bfloat16 or c.shape != shape or (B and c.stride(2) != 1):
-            raise ValueError(f"{name}: bf16 {list(shape)} with contiguous columns")
-    if k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must share their strides")
-    if positions.dtype != torch.int32 or positions.shape != (B,) or \
+    shape = (B, sinks + window, H_kv * d)
+    strides = k_cache.stride()
+    if k_cache.dtype is not bf16 or v_cache.dtype is not bf16 or k_cache.shape != shape or \
+            v_cache.shape != shape or v_cache.stride() != strides or (B and strides[2] != 1):
+        raise ValueError(f"k_cache and v_cache: bf16 {list(shape)}, contiguous columns, the same "
+                         "strides")
+    if positions.dtype is not torch.int32 or positions.shape != (B,) or \
             not positions.is_contiguous():
         raise ValueError("positions: contiguous int32 [B]")
     if out is None:
-        out = torch.empty((B, H * d), dtype=torch.bfloat16, device=q.device)
-    _rows2d("out", out, H * d, torch.bfloat16, B)
-    ld_cache = k_cache.stride(1) if shape[1] > 1 else max(k_cache.stride(1), shape[2])
+        out = torch.empty((B, H * d), dtype=bf16, device=q.device)
     _check(lib().vdn_sink_attn_step(
-        B, int(H), int(H_kv), int(d), int(window), int(sinks), _ptr(q), _ld(q), _ptr(k_new),
-        _ptr(v_new), _ld(k_new), _ptr(k_cache), _ptr(v_cache), ld_cache, k_cache.stride(0),
-        _ptr(positions), float(scale), _ptr(out), _ld(out), _stream(stream)),
-        "vdn_sink_attn_step")
+        B, H, H_kv, d, window, sinks, *_mat("q", q, B, H * d, bf16), knp, vnp, ld_new,
+        k_cache.data_ptr(), v_cache.data_ptr(), strides[1] if shape[1] > 1 else shape[2],
+        strides[0], positions.data_ptr(), scale, *_mat("out", out, B, H * d, bf16),
+        _raw_stream(stream, dev)), "vdn_sink_attn_step")
     return out
 
 
