@@ -7,17 +7,19 @@
 //   dQ_i = scale sum_j dS_ij k_j,   dK_j = scale sum_i dS_ij q_i
 // A query that saw nothing (lse = -inf) contributes nothing and gets dQ = 0.
 //
-// P is formed anew from q, k and lse.  Two passes, so that every sum has one
-// owner and a fixed order (the same call gives the same bits): the key pass
-// holds dK and dV of 128 keys of one key head and walks the queries of all its
-// query heads; the query pass holds dQ of 128 queries.  That is seven products
-// a pair of tiles where one pass with atomic adds into dQ would take five.
-// P and dS are rounded to bf16 for their products, sums stay fp32 in TMEM.
+// P is formed anew from q, k and lse.  Two passes, so that every sum has a
+// fixed order (the same call gives the same bits): the key pass holds dK and
+// dV of 128 keys of one key head and walks the queries of all its query heads;
+// the query pass holds dQ of 128 queries.  That is seven products a pair of
+// tiles where one pass with atomic adds into dQ would take five.  P and dS are
+// rounded to bf16 for their products, sums stay fp32 in TMEM.
 //
-// A sink key is seen by every later query, a key behind it by `window` of
-// them.  Where that leaves the few tiles with sinks far longer than the rest,
-// the queries past the window's reach are split over further CTAs whose fp32
-// sums the owner of the tile adds in order ("far" parts).
+// Key tiles differ in work: a sink is seen by every later query, other keys by
+// `window` of them, keys near a sequence's end by few.  The key pass therefore
+// deals out its items (a key tile with one query tile of one head) rather
+// than its tiles: every CTA takes the same number of consecutive items, and
+// where a tile's items end up with several CTAs each writes its fp32 part
+// and sink_join_kernel adds them in order.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -32,7 +34,13 @@ vdn_status sink_check(const vdn_sink_shape* shape, const void* q, int64_t ld_q, 
 
 namespace {
 
-constexpr int kThreads = 384;
+// Four softmax warpgroups, 32 columns of a 128 x 128 tile each: with one row a
+// thread that is 32 scores and 32 products in registers, and four warps a
+// scheduler to hide the tensor-memory round trips behind.  (Two warpgroups
+// with 64 columns: key pass 3800 cycles an item, the tensor pipe 45 % busy.)
+constexpr int kGroups = 4;
+constexpr int kThreads = 128 + kGroups * 128;
+constexpr int kCtas = 148;   // key pass CTAs at most: one an SM
 
 template <int DH>
 struct GradCfg {
@@ -59,7 +67,111 @@ struct StatsArgs {
   float* delta;
   void* zero[3];       // dq, dk, dv or null
   int64_t ld_zero[3];
+  struct SinkPlan* plan;
+  struct SlotRec* rec;
+  int64_t* before;
+  int ctas;            // at most
 };
+
+// How the key pass's items are dealt out, written by one block of the
+// statistics launch.  Slot s (a key tile of a sequence) has weight[s] items a
+// key head (1 for keys that no query sees: they get zeros), the unit (s, hk)
+// covers [Hkv before[s] + hk weight[s], ...) of `total` items, and CTA c of
+// `ctas` the items [total c / ctas, total (c + 1) / ctas).
+struct SlotRec {
+  int b, tile;     // sequence and its key tile
+  int t0, tiles;   // query tiles (of 128) that see it
+};
+
+struct SinkPlan {
+  int64_t total;
+  int ctas;
+  int start[kCtas];    // slot of each CTA's first item
+  SlotRec* rec;        // [slots]
+  int64_t* before;     // [slots + 1]
+};
+
+__device__ __forceinline__ int64_t plan_first(int64_t total, int ctas, int c) {
+  return total / ctas * c + total % ctas * c / ctas;
+}
+
+__device__ __forceinline__ SlotRec key_slot(const SinkDims& s, int slot) {
+  SlotRec r{0, -1, 0, 0};
+  r.b = sink_slot_seq(s.cu_k, s.B, s.Lk, 128, slot);
+  const int tile = slot - sink_slot_base(s.cu_k, r.b, s.Lk, 128);
+  const SinkSeq seq = sink_seq(s, r.b);
+  const int ks = 128 * tile, nq = seq.nq(), shift = seq.shift();
+  if (ks >= seq.nk()) return r;  // a slot without a tile
+  const int ke = min(ks + 127, seq.nk() - 1);
+  // queries [lo, hi) see a key of the tile
+  const int lo = max(0, ks - shift - s.m.ahead);
+  const int hi = ks < s.m.sinks ? nq : min(nq, ke - shift + s.m.window);
+  r.tile = tile;
+  r.t0 = lo / 128;
+  r.tiles = hi > lo ? (hi + 127) / 128 - r.t0 : 0;
+  return r;
+}
+
+// One block: the slots' records, their prefix sums and each CTA's first slot.
+__device__ void make_plan(const SinkDims& s, const StatsArgs& a) {
+  SinkPlan* p = a.plan;
+  __shared__ int64_t warp_sum[8];
+  __shared__ int64_t carry;
+  const int slots = sink_slots(s.Lk, s.B, 128), group = s.H / s.Hkv;
+  const int lane = lane_id(), warp = warp_id();
+  if (threadIdx.x == 0) carry = 0;
+  __syncthreads();
+  for (int base = 0; base < slots; base += 256) {
+    const int slot = base + threadIdx.x;
+    SlotRec r{0, -1, 0, 0};
+    if (slot < slots) {
+      r = key_slot(s, slot);
+      a.rec[slot] = r;
+    }
+    const int64_t w = r.tile < 0 ? 0 : max(1, r.tiles * group);
+    int64_t x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int64_t off = carry;
+    for (int i = 0; i < warp; ++i) off += warp_sum[i];
+    if (slot < slots) a.before[slot] = off + x - w;
+    __syncthreads();
+    if (threadIdx.x == 255) carry = off + x;
+    __syncthreads();
+  }
+  const int64_t total = carry * s.Hkv;
+  if (threadIdx.x == 0) a.before[slots] = carry;
+  // four items a CTA at least: loading a key tile and storing its sums costs
+  // about as much
+  int64_t n = total / 4;
+  n = n < 1 ? 1 : n > a.ctas ? a.ctas : n;
+  if (threadIdx.x == 0) {
+    p->total = total;
+    p->ctas = static_cast<int>(n);
+    p->rec = a.rec;
+    p->before = a.before;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < n; c += 256) {
+    // the last slot that begins at or before the CTA's first item and is not
+    // empty: empty ones begin where the next begins
+    const int64_t x = plan_first(total, static_cast<int>(n), c);
+    int lo = 0, hi = slots;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.before[mid] * s.Hkv <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    p->start[c] = lo;
+  }
+}
 
 constexpr int kStatsRows = 8;
 
@@ -72,14 +184,18 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
       if (a.zero[i] != nullptr)
         sink_zero_rest(dims.cu_k, dims.B, dims.Lk, a.zero[i], a.ld_zero[i], dims.Hkv * a.DH);
   }
-  const int slot = blockIdx.x / (128 / kStatsRows);
+  if (blockIdx.x == 0) {  // first, since it takes longest
+    make_plan(dims, a);
+    return;
+  }
+  const int blk = blockIdx.x - 1;
+  const int slot = blk / (128 / kStatsRows);
   const int slots = sink_slots(dims.Lq, dims.B, 128);
-  if (slot >= slots) return;
   const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
   const SinkSeq seq = sink_seq(dims, b);
   const int tile0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
   if (tile0 >= seq.q1) return;
-  const int first = blockIdx.x % (128 / kStatsRows) * kStatsRows;
+  const int first = blk % (128 / kStatsRows) * kStatsRows;
   const int lanes = a.DH / 8, step = 256 / lanes;
   const int lane = threadIdx.x % lanes, total = kStatsRows * dims.H;
   for (int base = threadIdx.x / lanes; base - static_cast<int>(threadIdx.x / lanes) < total;
@@ -121,16 +237,16 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
   }
 }
 
-// A operand (128 x 128 bf16 in TMEM, packed by the two warpgroups into words
-// [0, 32) and [64, 96) of its 128 columns) times 128 rows of `b_tile`
-// (MN-major), the half of the 128 that warpgroup w wrote.
+// A operand (128 x 128 bf16 in TMEM; warpgroup w packed its 32 columns into
+// words [32 w, 32 w + 16)) times 128 rows of `b_tile` (MN-major): the part
+// that warpgroup w wrote.
 template <int DH>
-__device__ __forceinline__ void grad_mma_half(uint32_t d, uint32_t a, uint32_t b_tile, int w,
+__device__ __forceinline__ void grad_mma_part(uint32_t d, uint32_t a, uint32_t b_tile, int w,
                                               bool accumulate) {
   constexpr uint32_t idesc = idesc_bf16(128, DH, false, true);
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
-    umma_ts(d, a + 64 * w + 8 * kk, sdesc_sw128(b_tile + (4 * w + kk) * 2048, 16384, 1024), idesc,
+  for (int kk = 0; kk < 2; ++kk)
+    umma_ts(d, a + 32 * w + 8 * kk, sdesc_sw128(b_tile + (2 * w + kk) * 2048, 16384, 1024), idesc,
             accumulate || w > 0 || kk > 0);
 }
 
@@ -149,9 +265,8 @@ __device__ __forceinline__ void grad_mma_scores(uint32_t d, uint32_t a_tile, uin
 // ---------------------------------------------------------------- key pass
 
 struct KeyPass {
-  int far_parts;      // 0: every tile walks all its queries
-  int far_tiles;      // tiles with sinks of a sequence, at most
-  float* far;         // [B, far_tiles, H_kv, far_parts, 2, DH, 128]
+  const SinkPlan* plan;
+  float* part;        // [ctas][2][dV, dK][DH][128]: a CTA's first and last tile where shared
   const float* nlse2;
   const float* delta;
   __nv_bfloat16* dk;
@@ -159,125 +274,46 @@ struct KeyPass {
   int64_t ld;
 };
 
-// The query tiles (128 queries, counted from the sequence's first) that see a
-// tile of keys [ks, ke]: `near` ones [n0, n1) and the far ones [n1, n2).
-struct KeyRange {
-  int n0, n1, n2;
-  __device__ void init(const SinkDims& s, const SinkSeq& seq, int ks, int ke) {
-    const int nq = seq.nq(), shift = seq.shift();
-    const int lo = max(0, ks - shift - s.m.ahead);
-    const int hi = min(nq, ke - shift + s.m.window);
-    n2 = (nq + 127) / 128;
-    n0 = min(lo / 128, n2);
-    n1 = max(n0, hi > 0 ? (hi + 127) / 128 : 0);
-    if (ks >= s.m.sinks) n2 = n1;
+// A CTA's walk over its units; every role keeps its own.
+struct KeyCursor {
+  int64_t x, x1;   // next item and end
+  int slot, hk;
+  SlotRec r;
+  int weight, i0, i1;
+  bool whole;
+  __device__ void init(const SinkPlan* p, int c) {
+    x = plan_first(p->total, p->ctas, c);
+    x1 = plan_first(p->total, p->ctas, c + 1);
+    slot = p->start[c] - 1;
+    hk = 0;
+    weight = 0;
+    r.tile = -1;
+  }
+  // The next unit; false at the end.
+  __device__ bool next(const SinkDims& s, const SinkPlan* p) {
+    if (x >= x1) return false;
+    if (weight == 0 || hk + 1 == s.Hkv) {
+      const bool first = weight == 0;
+      do {  // slots without a tile have no items
+        ++slot;
+        r = p->rec[slot];
+      } while (r.tile < 0);
+      weight = max(1, r.tiles * (s.H / s.Hkv));
+      hk = first ? static_cast<int>((x - p->before[slot] * s.Hkv) / weight) : 0;
+    } else {
+      ++hk;
+    }
+    const int64_t begin = p->before[slot] * s.Hkv + static_cast<int64_t>(hk) * weight;
+    i0 = static_cast<int>(x - begin);
+    i1 = static_cast<int>(min(static_cast<int64_t>(weight), x1 - begin));
+    whole = i0 == 0 && i1 == weight;
+    x = begin + i1;
+    if (r.tiles == 0) i1 = i0;  // a unit that no query sees
+    return true;
   }
 };
 
-// Softmax part of the key pass: thread = key row, this warpgroup's 64 of the
-// tile's 128 queries.  TMEM columns: S^T [0, 128), dP^T [128, 256).
 template <int DH>
-__device__ __forceinline__ bool key_pass_softmax(int w, uint32_t tmem, uint64_t* st_full,
-                                                 uint64_t* s_full, uint64_t* dp_full,
-                                                 uint64_t* p_ready, uint64_t* ds_ready,
-                                                 const uint8_t* stats, const SinkMask& m, int ks,
-                                                 int shift, int t0, int tiles, int i0, int i1,
-                                                 float scale_log2, uint64_t budget_ns) {
-  using Cfg = GradCfg<DH>;
-  const uint32_t quarter = warp_id() & 3;
-  const uint32_t lane_off = (quarter * 32) << 16;
-  const uint32_t s_addr = tmem + 64 * w + lane_off, dp_addr = s_addr + 128;
-  const int kw = ks + quarter * 32, key = kw + lane_id();
-  const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
-  for (int i = i0; i < i1; ++i) {
-    const int t = i - i0, s = t % Cfg::STAGES;
-    const int p0 = 128 * (t0 + i % tiles) + shift + 64 * w;  // position of this half's query 0
-    const bool edge = !sink_sees_all(m, p0, p0 + 63, kw, kw + 31);
-    const int c_lo = key - m.ahead - p0;                     // visible columns [c_lo, c_hi)
-    const int c_hi = key < m.sinks ? 64 : key - p0 + m.window;
-    const uint32_t see[2] = {sink_bits(c_lo, c_hi, 0), sink_bits(c_lo - 32, c_hi - 32, 0)};
-    if (!__all_sync(0xffffffffu, mbar_wait(&st_full[s], (t / Cfg::STAGES) & 1, budget_ns) &&
-                                     mbar_wait(s_full, t & 1, budget_ns)))
-      return false;
-    tc_fence_after();
-    const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(stats + s * Cfg::STATS) + 16 * w;
-    const ulonglong2* dl = nl + 32;
-    uint32_t x[64];
-    uint32_t (&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
-    uint32_t (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
-    tmem_ld32(s_addr, x0);
-    tmem_ld32(s_addr + 32, x1);
-    tmem_ld_wait();
-    reg_fence(x0);
-    reg_fence(x1);
-    // P over S in place: 2^(s scale log2 e - lse log2 e)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const ulonglong2 n2 = nl[e];
-      const uint64_t a = f32x2_fma((static_cast<uint64_t>(x[4 * e + 1]) << 32) | x[4 * e], cc, n2.x);
-      const uint64_t b =
-          f32x2_fma((static_cast<uint64_t>(x[4 * e + 3]) << 32) | x[4 * e + 2], cc, n2.y);
-      x[4 * e] = __float_as_uint(exp2_mufu(f32x2_lo(a)));
-      x[4 * e + 1] = __float_as_uint(exp2_mufu(f32x2_hi(a)));
-      x[4 * e + 2] = __float_as_uint(exp2_mufu(f32x2_lo(b)));
-      x[4 * e + 3] = __float_as_uint(exp2_mufu(f32x2_hi(b)));
-    }
-    if (edge) {
-#pragma unroll
-      for (int c = 0; c < 64; ++c) x[c] = see[c >> 5] & (1u << (c & 31)) ? x[c] : 0;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        pk[e] = pack_bf16x2(__uint_as_float(x[32 * q + 2 * e]),
-                            __uint_as_float(x[32 * q + 2 * e + 1]));
-      tmem_st16(s_addr + 16 * q, pk);
-    }
-    tmem_st_wait();
-    tc_fence_before();
-    mbar_arrive(&p_ready[w]);
-    // dS = P (dP - D)
-    if (!__all_sync(0xffffffffu, mbar_wait(dp_full, t & 1, budget_ns))) return false;
-    tc_fence_after();
-    uint32_t ds[32];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t g[32];
-      tmem_ld32(dp_addr + 32 * q, g);
-      tmem_ld_wait();
-      reg_fence(g);
-      if (edge) {  // dP of a hidden pair may be NaN, and 0 x NaN is not 0
-#pragma unroll
-        for (int c = 0; c < 32; ++c) g[c] = see[q] & (1u << c) ? g[c] : 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const ulonglong2 d2 = dl[8 * q + e];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const uint64_t d = f ? d2.y : d2.x;
-          const int c = 4 * e + 2 * f;
-          const float a = __uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - f32x2_lo(d));
-          const float b =
-              __uint_as_float(x[32 * q + c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d));
-          ds[16 * q + 2 * e + f] = pack_bf16x2(a, b);
-        }
-      }
-    }
-    // both halves of dP^T are in registers before dS goes over them
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      tmem_st16(dp_addr + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&ds[16 * q]));
-    tmem_st_wait();
-    tc_fence_before();
-    mbar_arrive(&ds_ready[w]);
-  }
-  return true;
-}
-
-template <int DH, bool FAR>
 __global__ void __launch_bounds__(kThreads, 1)
     sink_key_pass_kernel(const __grid_constant__ CUtensorMap qmap,
                          const __grid_constant__ CUtensorMap domap,
@@ -300,52 +336,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* do_empty = q_empty + Cfg::STAGES;   // [STAGES]
   uint64_t* s_full = do_empty + Cfg::STAGES;
   uint64_t* dp_full = s_full + 1;
-  uint64_t* p_ready = dp_full + 1;              // [2] one per warpgroup
-  uint64_t* ds_ready = p_ready + 2;             // [2]
-  uint64_t* mma_done = ds_ready + 2;
+  uint64_t* p_ready = dp_full + 1;              // [kGroups]
+  uint64_t* ds_ready = p_ready + kGroups;       // [kGroups]
+  uint64_t* acc_full = ds_ready + kGroups;      // a unit's sums are complete
+  uint64_t* acc_free = acc_full + 1;            // and have been read
+  uint64_t* mma_done = acc_free + 1;
   uint64_t* cut = mma_done + 1;                 // tiles whose last rows are zeroed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
 
-  // Ascending keys: without a window the first keys see the most queries.
-  const int lin = blockIdx.x;
-  const int hk = lin % dims.Hkv;
-  int b, tile, part = 0;
-  if (FAR) {
-    part = lin / dims.Hkv % a.far_parts;
-    const int t = lin / dims.Hkv / a.far_parts;
-    b = t / a.far_tiles;
-    tile = t % a.far_tiles;
-  } else {
-    const int slot = lin / dims.Hkv;
-    b = sink_slot_seq(dims.cu_k, dims.B, dims.Lk, 128, slot);
-    tile = slot - sink_slot_base(dims.cu_k, b, dims.Lk, 128);
-  }
-  const SinkSeq seq = sink_seq(dims, b);
-  const int ks = 128 * tile;
-  if (ks >= seq.nk() || (FAR && ks >= dims.m.sinks)) return;  // the whole CTA
-  const int ke = min(ks + 127, seq.nk() - 1);
-  const int key0 = seq.k0 + ks;
+  const int cta = blockIdx.x;
+  if (cta >= a.plan->ctas) return;
   const int group = dims.H / dims.Hkv;
-  KeyRange kr;
-  kr.init(dims, seq, ks, ke);
-  const bool split = a.far_parts > 0 && kr.n2 > kr.n1;
-  const int far_items = split ? (kr.n2 - kr.n1) * group : 0;
-  // items: query tiles t0 .. t0 + tiles of each query head in turn
-  const int t0 = FAR ? kr.n1 : kr.n0;
-  const int tiles = (FAR || !split ? kr.n2 : kr.n1) - t0;
-  int i0 = 0, i1 = tiles * group;
-  auto far_begin = [&](int f) {
-    return static_cast<int>(static_cast<int64_t>(far_items) * f / a.far_parts);
-  };
-  if (FAR) {
-    i0 = far_begin(part);
-    i1 = far_begin(part + 1);
-    if (i0 >= i1) return;  // the reader leaves it out by the same arithmetic
-  }
-  const int items = i1 - i0;
-  const int q_base = sink_slot_base(dims.cu_q, b, dims.Lq, 128);
   const int q_slots = sink_slots(dims.Lq, dims.B, 128);
   const uint32_t warp = warp_id();
+  KeyCursor cur;
+  cur.init(a.plan, cta);
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -358,10 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(s_full, 1);
     mbar_init(dp_full, 1);
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < kGroups; ++w) {
       mbar_init(&p_ready[w], 128);
       mbar_init(&ds_ready[w], 128);
     }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_free, kGroups * 128);
     mbar_init(mma_done, 1);
     mbar_init(cut, 1);
     fence_mbar_init();
@@ -377,84 +384,100 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // columns: S^T [0, 128), dP^T [128, 256), dV, dK
   const uint32_t tmem = *tmem_slot;
   const uint32_t dv_addr = tmem + 256, dk_addr = tmem + 256 + DH;
 
+  // Register split (launched with 96 x 640 = 61440): 128 * 64 + 512 * 104 =
+  // 61440.
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n" ::: "memory");
   }
   if (warp == 0) {
     // ================================================================ TMA
     const bool leader = lane_id() == 0;
-    if (leader) {
-      mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE);
-      for (int sl = 0; sl < Cfg::SLABS; ++sl) {
-        tma_load_2d(kvbuf + sl * 16384, &kmap, kv_full, hk * DH + 64 * sl, key0);
-        tma_load_2d(kvbuf + Cfg::TILE + sl * 16384, &vmap, kv_full, hk * DH + 64 * sl, key0);
-      }
-    }
-    int issued = 0, cuts = 0;
+    int n = 0, t = 0, cuts = 0;  // units, items and cut tiles so far
     bool ok = true;
-    for (int i = i0; i < i1; ++i) {
-      const int t = i - i0, s = t % Cfg::STAGES;
-      const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
-      const int qt = t0 + i % tiles, h = hk * group + i / tiles;
-      const int row = seq.q0 + 128 * qt, valid = min(128, seq.nq() - 128 * qt);
-      uint8_t* qb = ring + s * 2 * Cfg::TILE;
-      uint8_t* dob = qb + Cfg::TILE;
-      if (t >= Cfg::STAGES &&
-          !__all_sync(0xffffffffu, mbar_wait(&q_empty[s], par, budget_ns))) {
+    while (ok && cur.next(dims, a.plan)) {
+      const SinkSeq seq = sink_seq(dims, cur.r.b);
+      const int q_base = sink_slot_base(dims.cu_q, cur.r.b, dims.Lq, 128);
+      const int key0 = seq.k0 + 128 * cur.r.tile;
+      // the last unit's products have read K and V
+      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(acc_full, (n - 1) & 1, budget_ns))) {
         ok = false;
         break;
       }
-      uint64_t* qbar = valid < 128 ? cut : &q_full[s];
       if (leader) {
-        mbar_arrive_expect_tx(&st_full[s], Cfg::STATS);
-        const int64_t at = (static_cast<int64_t>(h) * q_slots + q_base + qt) * 128;
-        bulk_load(stats + s * Cfg::STATS, a.nlse2 + at, 512, &st_full[s]);
-        bulk_load(stats + s * Cfg::STATS + 512, a.delta + at, 512, &st_full[s]);
-        mbar_arrive_expect_tx(qbar, (valid < 128 ? 2 : 1) * Cfg::TILE);
-        for (int sl = 0; sl < Cfg::SLABS; ++sl)
-          tma_load_2d(qb + sl * 16384, &qmap, qbar, h * DH + 64 * sl, row);
+        mbar_arrive_expect_tx(kv_full, 2 * Cfg::TILE);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl) {
+          tma_load_2d(kvbuf + sl * 16384, &kmap, kv_full, cur.hk * DH + 64 * sl, key0);
+          tma_load_2d(kvbuf + Cfg::TILE + sl * 16384, &vmap, kv_full, cur.hk * DH + 64 * sl,
+                      key0);
+        }
       }
       __syncwarp();
-      ++issued;
-      if (t >= Cfg::STAGES &&
-          !__all_sync(0xffffffffu, mbar_wait(&do_empty[s], par, budget_ns))) {
-        ok = false;
-        break;
-      }
-      uint64_t* dobar = valid < 128 ? cut : &do_full[s];
-      if (leader) {
-        if (valid == 128) mbar_arrive_expect_tx(dobar, Cfg::TILE);
-        for (int sl = 0; sl < Cfg::SLABS; ++sl)
-          tma_load_2d(dob + sl * 16384, &domap, dobar, h * DH + 64 * sl, row);
-      }
-      __syncwarp();
-      if (valid < 128) {
-        // queries past the sequence's end have P = 0; their rows must not
-        // be NaN
-        if (!__all_sync(0xffffffffu, mbar_wait(cut, cuts & 1, budget_ns))) {
+      ++n;
+      for (int i = cur.i0; i < cur.i1; ++i) {
+        const int s = t % Cfg::STAGES;
+        const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
+        const int qt = cur.r.t0 + i % cur.r.tiles, h = cur.hk * group + i / cur.r.tiles;
+        const int row = seq.q0 + 128 * qt, valid = min(128, seq.nq() - 128 * qt);
+        uint8_t* qb = ring + s * 2 * Cfg::TILE;
+        uint8_t* dob = qb + Cfg::TILE;
+        if (t >= Cfg::STAGES &&
+            !__all_sync(0xffffffffu, mbar_wait(&q_empty[s], par, budget_ns))) {
           ok = false;
           break;
         }
-        ++cuts;
-        sink_zero_rows(qb, Cfg::SLABS, valid);
-        sink_zero_rows(dob, Cfg::SLABS, valid);
+        uint64_t* qbar = valid < 128 ? cut : &q_full[s];
         if (leader) {
-          mbar_arrive(&q_full[s]);
-          mbar_arrive(&do_full[s]);
+          mbar_arrive_expect_tx(&st_full[s], Cfg::STATS);
+          const int64_t at = (static_cast<int64_t>(h) * q_slots + q_base + qt) * 128;
+          bulk_load(stats + s * Cfg::STATS, a.nlse2 + at, 512, &st_full[s]);
+          bulk_load(stats + s * Cfg::STATS + 512, a.delta + at, 512, &st_full[s]);
+          mbar_arrive_expect_tx(qbar, (valid < 128 ? 2 : 1) * Cfg::TILE);
+          for (int sl = 0; sl < Cfg::SLABS; ++sl)
+            tma_load_2d(qb + sl * 16384, &qmap, qbar, h * DH + 64 * sl, row);
+        }
+        __syncwarp();
+        ++t;
+        if (t > Cfg::STAGES &&
+            !__all_sync(0xffffffffu, mbar_wait(&do_empty[s], par, budget_ns))) {
+          ok = false;
+          break;
+        }
+        uint64_t* dobar = valid < 128 ? cut : &do_full[s];
+        if (leader) {
+          if (valid == 128) mbar_arrive_expect_tx(dobar, Cfg::TILE);
+          for (int sl = 0; sl < Cfg::SLABS; ++sl)
+            tma_load_2d(dob + sl * 16384, &domap, dobar, h * DH + 64 * sl, row);
+        }
+        __syncwarp();
+        if (valid < 128) {
+          // queries past the sequence's end have P = 0; their rows must not
+          // be NaN
+          if (!__all_sync(0xffffffffu, mbar_wait(cut, cuts & 1, budget_ns))) {
+            ok = false;
+            break;
+          }
+          ++cuts;
+          sink_zero_rows(qb, Cfg::SLABS, valid);
+          sink_zero_rows(dob, Cfg::SLABS, valid);
+          if (leader) {
+            mbar_arrive(&q_full[s]);
+            mbar_arrive(&do_full[s]);
+          }
         }
       }
     }
     if (!ok) record_status(status, kStatusTimeout);
     // no load may be in flight when the CTA ends
-    mbar_wait(kv_full, 0, 200000000ull);
-    for (int t = max(0, issued - Cfg::STAGES); t < issued; ++t) {
-      const uint32_t par = (t / Cfg::STAGES) & 1;
-      mbar_wait(&st_full[t % Cfg::STAGES], par, 200000000ull);
-      mbar_wait(&q_full[t % Cfg::STAGES], par, 200000000ull);
-      mbar_wait(&do_full[t % Cfg::STAGES], par, 200000000ull);
+    if (n > 0) mbar_wait(kv_full, (n - 1) & 1, 200000000ull);
+    for (int u = max(0, t - Cfg::STAGES); u < t; ++u) {
+      const uint32_t par = (u / Cfg::STAGES) & 1;
+      mbar_wait(&st_full[u % Cfg::STAGES], par, 200000000ull);
+      mbar_wait(&q_full[u % Cfg::STAGES], par, 200000000ull);
+      mbar_wait(&do_full[u % Cfg::STAGES], par, 200000000ull);
     }
     if (!ok) mbar_wait(cut, cuts & 1, 200000000ull);  // a cut tile's loads may be in flight
   } else if (warp == 1) {
@@ -479,54 +502,159 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit(dp_full);
         return true;
       };
-      // dV += P^T dO or dK += dS^T Q, each half as its warpgroup is done
-      auto sums = [&](uint64_t* ready, uint32_t d, uint32_t at, uint32_t tile, int t) {
-        for (int w = 0; w < 2; ++w) {
+      // dV += P^T dO or dK += dS^T Q, each part as its warpgroup is done
+      auto sums = [&](uint64_t* ready, uint32_t d, uint32_t at, uint32_t tile, int t, bool more) {
+        for (int w = 0; w < kGroups; ++w) {
           if (!mbar_wait(&ready[w], t & 1, budget_ns)) return false;
           tc_fence_after();
-          grad_mma_half<DH>(d, at, tile, w, t > 0);
+          grad_mma_part<DH>(d, at, tile, w, more);
         }
         return true;
       };
-      bool ok = mbar_wait(kv_full, 0, budget_ns);
-      if (ok && items > 0) ok = scores(0) && d_scores(0);
-      // While the tensor core runs dV_t and S_{t+1}, the warpgroups form dS_t;
-      // while it runs dK_t and dP_{t+1}, they form P_{t+1}.
-      for (int t = 0; t < items && ok; ++t) {
-        ok = sums(p_ready, dv_addr, tmem, q_tile(t) + Cfg::TILE, t);
+      int n = 0, t = 0;
+      bool ok = true;
+      while (ok && cur.next(dims, a.plan)) {
+        const int items = cur.i1 - cur.i0;
+        if (!(ok = mbar_wait(kv_full, n & 1, budget_ns))) break;
+        tc_fence_after();
+        if (items > 0 && !(ok = scores(t) && d_scores(t))) break;
+        // the last unit's sums have been read
+        if (n > 0 && !(ok = mbar_wait(acc_free, (n - 1) & 1, budget_ns))) break;
+        tc_fence_after();
+        // While the tensor core runs dV_t and S_{t+1}, the warpgroups form
+        // dS_t; while it runs dK_t and dP_{t+1}, they form P_{t+1}.
+        for (int i = 0; i < items; ++i, ++t) {
+          const bool more = i + 1 < items;
+          if (!(ok = sums(p_ready, dv_addr, tmem, q_tile(t) + Cfg::TILE, t, i > 0))) break;
+          umma_commit(&do_empty[t % Cfg::STAGES]);
+          if (more && !(ok = scores(t + 1))) break;
+          if (!(ok = sums(ds_ready, dk_addr, tmem + 128, q_tile(t), t, i > 0))) break;
+          umma_commit(&q_empty[t % Cfg::STAGES]);
+          if (more && !(ok = d_scores(t + 1))) break;
+        }
         if (!ok) break;
-        umma_commit(&do_empty[t % Cfg::STAGES]);
-        if (t + 1 < items && !(ok = scores(t + 1))) break;
-        ok = sums(ds_ready, dk_addr, tmem + 128, q_tile(t), t);
-        if (!ok) break;
-        umma_commit(&q_empty[t % Cfg::STAGES]);
-        if (t + 1 < items) ok = d_scores(t + 1);
+        umma_commit(acc_full);
+        ++n;
       }
       if (!ok) record_status(status, kStatusTimeout);
       umma_commit(mma_done);
     }
   } else if (warp >= 4) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n" ::: "memory");
+    // thread = key row; this warpgroup's 32 of the tile's 128 queries
     const int w = (warp - 4) >> 2;
-    const bool ok = key_pass_softmax<DH>(w, tmem, st_full, s_full, dp_full, p_ready, ds_ready,
-                                         stats, dims.m, ks, seq.shift(), t0, tiles, i0, i1,
-                                         scale * 1.4426950408889634f, budget_ns);
-    // warpgroup 0 stores dV, warpgroup 1 dK
-    if (__all_sync(0xffffffffu, ok && mbar_wait(mma_done, 0, budget_ns))) {
-      tc_fence_after();
-      const int row = (warp & 3) * 32 + lane_id();
-      const uint32_t addr = (w ? dk_addr : dv_addr) + (((warp & 3) * 32) << 16);
-      const float factor = w ? scale : 1.f;
-      const int64_t far_at =
-          (((static_cast<int64_t>(b) * a.far_tiles + tile) * dims.Hkv + hk) * a.far_parts) * 2 + w;
-      __nv_bfloat16* dst = (w ? a.dk : a.dv) + static_cast<int64_t>(key0 + row) * a.ld + hk * DH;
-      const bool live = ks + row <= ke && in_bounds(status, key0 + row, dims.Lk, hk * DH, DH,
-                                                    static_cast<int64_t>(dims.Hkv) * DH);
-#pragma unroll 1
-      for (int c = 0; c < DH; c += 32) {
+    const uint32_t quarter = warp & 3, lane_off = (quarter * 32) << 16;
+    const uint32_t s_addr = tmem + 32 * w + lane_off, dp_addr = s_addr + 128;
+    const float scale_log2 = scale * 1.4426950408889634f;
+    const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
+    const SinkMask m = dims.m;
+    int n = 0, t = 0;
+    bool ok = true;
+    while (ok && cur.next(dims, a.plan)) {
+      const SinkSeq seq = sink_seq(dims, cur.r.b);
+      const int ks = 128 * cur.r.tile, kw = ks + quarter * 32, key = kw + lane_id();
+      for (int i = cur.i0; i < cur.i1; ++i, ++t) {
+        const int s = t % Cfg::STAGES;
+        // position of this part's first query
+        const int p0 = 128 * (cur.r.t0 + i % cur.r.tiles) + seq.shift() + 32 * w;
+        const bool edge = !sink_sees_all(m, p0, p0 + 31, kw, kw + 31);
+        const uint32_t see = sink_bits(key - m.ahead - p0,
+                                       key < m.sinks ? 32 : key - p0 + m.window, 0);
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&st_full[s], (t / Cfg::STAGES) & 1, budget_ns) &&
+                            mbar_wait(s_full, t & 1, budget_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(stats + s * Cfg::STATS) + 8 * w;
+        const ulonglong2* dl = nl + 32;
         uint32_t x[32];
-        if (items > 0) {
+        tmem_ld32(s_addr, x);
+        tmem_ld_wait();
+        reg_fence(x);
+        // P over S: 2^(s scale log2 e - lse log2 e)
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const ulonglong2 n2 = nl[e];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const int c = 4 * e + 2 * f;
+            const uint64_t y = f32x2_fma((static_cast<uint64_t>(x[c + 1]) << 32) | x[c], cc,
+                                         f ? n2.y : n2.x);
+            x[c] = __float_as_uint(exp2_mufu(f32x2_lo(y)));
+            x[c + 1] = __float_as_uint(exp2_mufu(f32x2_hi(y)));
+          }
+        }
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = see & (1u << c) ? x[c] : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          pk[e] = pack_bf16x2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1]));
+        tmem_st16(s_addr, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_ready[w]);
+        // dS = P (dP - D)
+        if (!__all_sync(0xffffffffu, mbar_wait(dp_full, t & 1, budget_ns))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t g[32];
+        tmem_ld32(dp_addr, g);
+        tmem_ld_wait();
+        reg_fence(g);
+        if (edge) {  // dP of a hidden pair may be NaN, and 0 x NaN is not 0
+#pragma unroll
+          for (int c = 0; c < 32; ++c) g[c] = see & (1u << c) ? g[c] : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const ulonglong2 d2 = dl[e];
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const uint64_t d = f ? d2.y : d2.x;
+            const int c = 4 * e + 2 * f;
+            pk[2 * e + f] = pack_bf16x2(
+                __uint_as_float(x[c]) * (__uint_as_float(g[c]) - f32x2_lo(d)),
+                __uint_as_float(x[c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d)));
+          }
+        }
+        tmem_st16(dp_addr, pk);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&ds_ready[w]);
+      }
+      if (!ok) break;
+      // ---- the unit's sums: warpgroups 0, 1 store dV, 2, 3 dK, half the
+      // columns each
+      if (!__all_sync(0xffffffffu, mbar_wait(acc_full, n & 1, budget_ns))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const int which = w >> 1, c0 = (w & 1) * (DH / 2);
+      const uint32_t addr = (which ? dk_addr : dv_addr) + lane_off + c0;
+      const float factor = which ? scale : 1.f;
+      const int row = quarter * 32 + lane_id();
+      const int key0 = seq.k0 + ks;
+      const bool live = ks + row < seq.nk() &&
+                        in_bounds(status, key0 + row, dims.Lk, cur.hk * DH, DH,
+                                  static_cast<int64_t>(dims.Hkv) * DH);
+      __nv_bfloat16* dst = (which ? a.dk : a.dv) + static_cast<int64_t>(key0 + row) * a.ld +
+                           cur.hk * DH + c0;
+      float* part = a.part +
+                    ((static_cast<int64_t>(cta) * 2 + (cur.i0 == 0)) * 2 + which) * (DH * 128) +
+                    c0 * 128 + row;
+#pragma unroll 1
+      for (int c = 0; c < DH / 2; c += 32) {
+        uint32_t x[32];
+        if (cur.i1 > cur.i0) {
           tmem_ld32(addr + c, x);
           tmem_ld_wait();
           reg_fence(x);
@@ -534,36 +662,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = 0;
         }
-        if (FAR) {
-          float* out = a.far + (far_at + 2 * part) * (DH * 128) + c * 128 + row;
+        if (!cur.whole) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) out[e * 128] = __uint_as_float(x[e]);
-          continue;
-        }
-        if (split) {
-          for (int f = 0; f < a.far_parts; ++f) {
-            if (far_begin(f) >= far_begin(f + 1)) continue;
-            const float* in = a.far + (far_at + 2 * f) * (DH * 128) + c * 128 + row;
+          for (int e = 0; e < 32; ++e) part[(c + e) * 128] = __uint_as_float(x[e]);
+        } else if (live) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              x[e] = __float_as_uint(__uint_as_float(x[e]) + in[e * 128]);
+          for (int e = 0; e < 32; e += 8) {
+            uint4 u;
+            auto two = [&](int k) {
+              return pack_bf16x2(__uint_as_float(x[e + k]) * factor,
+                                 __uint_as_float(x[e + k + 1]) * factor);
+            };
+            u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
+            *reinterpret_cast<uint4*>(dst + c + e) = u;
           }
         }
-        if (!live) continue;
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 u;
-          auto two = [&](int n) {
-            return pack_bf16x2(__uint_as_float(x[e + n]) * factor,
-                               __uint_as_float(x[e + n + 1]) * factor);
-          };
-          u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
-          *reinterpret_cast<uint4*>(dst + c + e) = u;
-        }
       }
-    } else {
-      record_status(status, kStatusTimeout);
+      tc_fence_before();
+      mbar_arrive(acc_free);
+      ++n;
     }
+    if (!ok) record_status(status, kStatusTimeout);
   }
 
   tc_fence_before();
@@ -572,6 +691,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     mbar_wait(mma_done, 0, 200000000ull);
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// dK and dV of the units that several CTAs share: the sum of their parts, the
+// CTA with the unit's first items first.  A block: 32 columns of one of them.
+template <int DH>
+__global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, const KeyPass a,
+                                                        float scale) {
+  const SinkPlan* p = a.plan;
+  const int slot = blockIdx.x / dims.Hkv, hk = blockIdx.x % dims.Hkv;
+  const SlotRec r = p->rec[slot];
+  if (r.tile < 0) return;
+  const int64_t weight = max(1, r.tiles * (dims.H / dims.Hkv));
+  const int64_t begin = p->before[slot] * dims.Hkv + hk * weight, last = begin + weight - 1;
+  auto owner = [&](int64_t x) {  // the CTA of item x
+    int c = static_cast<int>(static_cast<double>(x) * p->ctas / static_cast<double>(p->total));
+    c = min(c, p->ctas - 1);
+    while (c > 0 && plan_first(p->total, p->ctas, c) > x) --c;
+    while (c + 1 < p->ctas && plan_first(p->total, p->ctas, c + 1) <= x) ++c;
+    return c;
+  };
+  const int first = owner(begin), end = owner(last);
+  if (first == end) return;
+  const SinkSeq seq = sink_seq(dims, r.b);
+  constexpr int BLOCKS = DH / 32;
+  const int which = blockIdx.y / BLOCKS, c0 = blockIdx.y % BLOCKS * 32;
+  const int row = threadIdx.x & 127, c1 = c0 + (threadIdx.x >> 7) * 16;
+  float x[16] = {};
+  for (int c = first; c <= end; ++c) {
+    const float* in = a.part + ((static_cast<int64_t>(c) * 2 + (c == first)) * 2 + which) *
+                                   (DH * 128) + c1 * 128 + row;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] += in[e * 128];
+  }
+  if (128 * r.tile + row >= seq.nk()) return;
+  const float f = which ? scale : 1.f;
+  __nv_bfloat16* dst = (which ? a.dk : a.dv) +
+                       static_cast<int64_t>(seq.k0 + 128 * r.tile + row) * a.ld + hk * DH + c1;
+#pragma unroll
+  for (int e = 0; e < 16; e += 8) {
+    uint4 u;
+    u.x = pack_bf16x2(x[e] * f, x[e + 1] * f);
+    u.y = pack_bf16x2(x[e + 2] * f, x[e + 3] * f);
+    u.z = pack_bf16x2(x[e + 4] * f, x[e + 5] * f);
+    u.w = pack_bf16x2(x[e + 6] * f, x[e + 7] * f);
+    *reinterpret_cast<uint4*>(dst + e) = u;
   }
 }
 
@@ -603,10 +768,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* k_empty = v_full + Cfg::STAGES;   // [STAGES]
   uint64_t* v_empty = k_empty + Cfg::STAGES;  // [STAGES]
   uint64_t* s_full = v_empty + Cfg::STAGES;
-  uint64_t* s_free = s_full + 1;              // S loaded by all 256 threads
+  uint64_t* s_free = s_full + 1;              // S loaded by all softmax threads
   uint64_t* dp_full = s_free + 1;             // [2]
-  uint64_t* ds_ready = dp_full + 2;           // [2] one per warpgroup
-  uint64_t* mma_done = ds_ready + 2;
+  // [2][kGroups], by the parity of the key tile: a warpgroup may be done with
+  // tile j + 1 before the products of tile j have waited for the slowest one
+  uint64_t* ds_ready = dp_full + 2;
+  uint64_t* mma_done = ds_ready + 2 * kGroups;
   uint64_t* cut = mma_done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
 
@@ -632,11 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_empty[s], 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, 256);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&dp_full[w], 1);
-      mbar_init(&ds_ready[w], 128);
-    }
+    mbar_init(s_free, kGroups * 128);
+    mbar_init(&dp_full[0], 1);
+    mbar_init(&dp_full[1], 1);
+    for (int w = 0; w < 2 * kGroups; ++w) mbar_init(&ds_ready[w], 128);
     mbar_init(mma_done, 1);
     mbar_init(cut, 1);
     fence_mbar_init();
@@ -656,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t dq_addr = tmem + 384;
 
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;\n" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n" ::: "memory");
   }
   if (warp == 0) {
     // ================================================================ TMA
@@ -742,10 +908,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (!(ok = products(j + 1))) break;
         }
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (!(ok = mbar_wait(&ds_ready[w], j & 1, budget_ns))) break;
+        for (int w = 0; w < kGroups && ok; ++w) {
+          if (!(ok = mbar_wait(&ds_ready[(j & 1) * kGroups + w], (j >> 1) & 1, budget_ns))) break;
           tc_fence_after();
-          grad_mma_half<DH>(dq_addr, tmem + 128 + 128 * (j & 1), k_tile(j), w, j > 0);
+          grad_mma_part<DH>(dq_addr, tmem + 128 + 128 * (j & 1), k_tile(j), w, j > 0);
         }
         if (ok) umma_commit(&k_empty[j % Cfg::STAGES]);
       }
@@ -754,8 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ================================================================ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
-    const int w = (warp - 4) >> 2;           // this warpgroup's 64 keys of a tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n" ::: "memory");
+    const int w = (warp - 4) >> 2;           // this warpgroup's 32 keys of a tile
     const uint32_t quarter = warp & 3;
     const uint32_t lane_off = (quarter * 32) << 16;
     const int row = quarter * 32 + lane_id();
@@ -766,60 +932,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const SinkMask m = dims.m;
     bool ok = true;
     for (int j = 0; j < kt.n; ++j) {
-      const int ks = kt.start(j) + 64 * w, valid = kt.valid(j) - 64 * w;
-      const bool edge = valid < 64 || !sink_sees_all(m, pw, pw + 31, ks, ks + 63);
-      const int c_end = min(valid, p + m.ahead + 1 - ks);
-      const int c_win = p - m.window + 1 - ks, c_sink = m.sinks - ks;
-      const uint32_t see[2] = {sink_bits(c_win, c_end, c_sink),
-                               sink_bits(c_win - 32, c_end - 32, c_sink - 32)};
+      const int ks = kt.start(j) + 32 * w, valid = kt.valid(j) - 32 * w;
+      const bool edge = valid < 32 || !sink_sees_all(m, pw, pw + 31, ks, ks + 31);
+      const uint32_t see = sink_bits(p - m.window + 1 - ks, min(valid, p + m.ahead + 1 - ks),
+                                     m.sinks - ks);
       if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, budget_ns))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      uint32_t x[64];
-      uint32_t (&x0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[0]);
-      uint32_t (&x1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&x[32]);
-      tmem_ld32(tmem + lane_off + 64 * w, x0);
-      tmem_ld32(tmem + lane_off + 64 * w + 32, x1);
+      uint32_t x[32];
+      tmem_ld32(tmem + lane_off + 32 * w, x);
       tmem_ld_wait();
-      reg_fence(x0);
-      reg_fence(x1);
+      reg_fence(x);
       tc_fence_before();
       mbar_arrive(s_free);
 #pragma unroll
-      for (int c = 0; c < 64; ++c)
+      for (int c = 0; c < 32; ++c)
         x[c] = __float_as_uint(exp2_mufu(fmaf(__uint_as_float(x[c]), scale_log2, nl)));
       if (!__all_sync(0xffffffffu, mbar_wait(&dp_full[j & 1], (j >> 1) & 1, budget_ns))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t g_addr = tmem + 128 + 128 * (j & 1) + 64 * w + lane_off;
-      uint32_t ds[32];
+      const uint32_t g_addr = tmem + 128 + 128 * (j & 1) + 32 * w + lane_off;
+      uint32_t g[32];
+      tmem_ld32(g_addr, g);
+      tmem_ld_wait();
+      reg_fence(g);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t g[32];
-        tmem_ld32(g_addr + 32 * q, g);
-        tmem_ld_wait();
-        reg_fence(g);
+      for (int c = 0; c < 32; ++c)
+        g[c] = __float_as_uint(__uint_as_float(x[c]) * (__uint_as_float(g[c]) - dl));
+      if (edge) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-          g[c] = __float_as_uint(__uint_as_float(x[32 * q + c]) * (__uint_as_float(g[c]) - dl));
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) g[c] = see[q] & (1u << c) ? g[c] : 0;
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          ds[16 * q + e] = pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+        for (int c = 0; c < 32; ++c) g[c] = see & (1u << c) ? g[c] : 0;
       }
+      uint32_t ds[16];
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        tmem_st16(g_addr + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&ds[16 * q]));
+      for (int e = 0; e < 16; ++e)
+        ds[e] = pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+      tmem_st16(g_addr, ds);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&ds_ready[w]);
+      mbar_arrive(&ds_ready[(j & 1) * kGroups + w]);
     }
     if (__all_sync(0xffffffffu, ok && mbar_wait(mma_done, 0, budget_ns))) {
       tc_fence_after();
@@ -827,9 +982,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         in_bounds(status, row0 + row, dims.Lq, h * DH, DH,
                                   static_cast<int64_t>(dims.H) * DH);
       __nv_bfloat16* dst = dq + static_cast<int64_t>(row0 + row) * ld_dq + h * DH;
-      // each warpgroup stores half the columns
+      // the warpgroups take the 32-column parts in turn
 #pragma unroll 1
-      for (int c = w * (DH / 2); c < (w + 1) * (DH / 2); c += 32) {
+      for (int c = 32 * w; c < DH; c += 32 * kGroups) {
         uint32_t x[32];
         if (kt.n > 0) {
           tmem_ld32(dq_addr + lane_off + c, x);
@@ -867,44 +1022,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- host
 
-// Far parts: only where sequences can be more than twice as long as what a
-// plain key tile walks, and the tiles with sinks alone leave SMs idle; then
-// about two CTAs an SM over all of them, eight query tiles at least each.
-struct FarPlan {
-  int parts, tiles;
-};
-
-FarPlan far_plan(const vdn_sink_shape& s) {
-  FarPlan f{0, 0};
-  const int longest = s.Lq < s.Lk ? s.Lq : s.Lk;
-  if (s.sinks == 0 || longest == 0) return f;
-  const int sinks = s.sinks < s.Lk ? s.sinks : s.Lk;
-  f.tiles = (sinks + 127) / 128;
-  const int64_t owners = static_cast<int64_t>(s.B) * f.tiles * s.H_kv;
-  if (static_cast<int64_t>(s.Lq) <= 2 * (static_cast<int64_t>(s.window) + s.ahead + 256) ||
-      owners >= 148)
-    return FarPlan{0, 0};
-  const int64_t most = static_cast<int64_t>(s.Lq) / 128 * (s.H / s.H_kv) / 8;
-  int64_t n = 2 * 148 / owners;
-  n = n > most ? most : n;
-  n = n > 32 ? 32 : n;
-  f.parts = n < 1 ? 0 : static_cast<int>(n);
-  return f;
-}
-
+// Workspace: status, the two statistics, the plan with its arrays, the parts
+// of shared units.
 struct GradLayout {
   size_t stats;  // bytes of one statistic
-  FarPlan far;
+  size_t plan, rec, before, part;
+  int ctas;
   size_t total;
 };
 
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
 GradLayout grad_layout(const vdn_sink_shape& s) {
   GradLayout l;
-  l.stats = static_cast<size_t>(s.H) * sink_slots(s.Lq, s.B, 128) * 128 * sizeof(float);
-  l.far = far_plan(s);
-  l.total = kStatusBytes + 2 * l.stats +
-            static_cast<size_t>(s.B) * l.far.tiles * s.H_kv * l.far.parts * 2 * s.d * 128 *
-                sizeof(float);
+  const size_t k_slots = sink_slots(s.Lk, s.B, 128);
+  // no more CTAs than four items each could make: a tile has at most
+  // (Lq + 127) / 128 + 1 query tiles of each of its heads
+  const double items = static_cast<double>(k_slots) * s.H * (s.Lq / 128 + 2) / 4;
+  l.ctas = items < 1 ? 1 : items > kCtas ? kCtas : static_cast<int>(items);
+  l.stats = align256(static_cast<size_t>(s.H) * sink_slots(s.Lq, s.B, 128) * 128 * sizeof(float));
+  l.plan = kStatusBytes + 2 * l.stats;
+  l.rec = l.plan + align256(sizeof(SinkPlan));
+  l.before = l.rec + align256(k_slots * sizeof(SlotRec));
+  l.part = l.before + align256((k_slots + 1) * sizeof(int64_t));
+  l.total = l.part + static_cast<size_t>(l.ctas) * 4 * s.d * 128 * sizeof(float);
   return l;
 }
 
@@ -914,31 +1055,27 @@ struct GradMaps {
 
 template <int DH>
 cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const GradMaps& t,
-                             const FarPlan& far, const KeyPass& a, const StatsArgs& st,
-                             float scale, __nv_bfloat16* dq, int64_t ld_dq) {
+                             const KeyPass& a, int ctas, const StatsArgs& st, float scale,
+                             __nv_bfloat16* dq, int64_t ld_dq) {
   using Cfg = GradCfg<DH>;
-  static std::atomic<uint64_t> set_near{0}, set_far{0}, set_query{0};
-  if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, false>, Cfg::SMEM, set_near)) return e;
-  if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH, true>, Cfg::SMEM, set_far)) return e;
+  static std::atomic<uint64_t> set_key{0}, set_query{0};
+  if (cudaError_t e = set_smem_once(sink_key_pass_kernel<DH>, Cfg::SMEM, set_key)) return e;
   if (cudaError_t e = set_smem_once(sink_query_pass_kernel<DH>, Cfg::SMEM, set_query)) return e;
   const int q_slots = sink_slots(dims.Lq, dims.B, 128);
-  sink_stats_kernel<<<128 / kStatsRows * q_slots, 256, 0, ctx.stream>>>(dims, st);
+  sink_stats_kernel<<<1 + 128 / kStatsRows * q_slots, 256, 0, ctx.stream>>>(dims, st);
   if (cudaError_t e = cudaGetLastError()) return e;
-  if (far.parts > 0) {
-    sink_key_pass_kernel<DH, true>
-        <<<dims.B * far.tiles * dims.Hkv * far.parts, kThreads, Cfg::SMEM, ctx.stream>>>(
-            t.q, t.d_o, t.k, t.v, dims, a, scale, ctx.status, ctx.budget_ns);
-    if (cudaError_t e = cudaGetLastError()) return e;
-  }
   if (dims.Lk > 0) {
-    sink_key_pass_kernel<DH, false><<<sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, kThreads,
-                                      Cfg::SMEM, ctx.stream>>>(t.q, t.d_o, t.k, t.v, dims, a,
-                                                               scale, ctx.status, ctx.budget_ns);
+    sink_key_pass_kernel<DH><<<ctas, kThreads, Cfg::SMEM, ctx.stream>>>(
+        t.q, t.d_o, t.k, t.v, dims, a, scale, ctx.status, ctx.budget_ns);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    sink_join_kernel<DH><<<dim3(sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, DH / 16), 256, 0,
+                           ctx.stream>>>(dims, a, scale);
     if (cudaError_t e = cudaGetLastError()) return e;
   }
   if (dims.Lq > 0)
     sink_query_pass_kernel<DH><<<q_slots * dims.H, kThreads, Cfg::SMEM, ctx.stream>>>(
-        t.q, t.d_o, t.k, t.v, dims, a.nlse2, a.delta, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
+        t.q, t.d_o, t.k, t.v, dims, a.nlse2, a.delta, scale, dq, ld_dq, ctx.status,
+        ctx.budget_ns);
   return cudaGetLastError();
 }
 
@@ -1000,17 +1137,17 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
     return VDN_ERR_CUDA;
   if (s.Lq == 0) t.q = t.d_o = t.k;
   if (s.Lk == 0) t.k = t.v = t.q;
-  uint8_t* base = static_cast<uint8_t*>(ws) + kStatusBytes;
-  float* nlse2 = reinterpret_cast<float*>(base);
-  float* delta = reinterpret_cast<float*>(base + lay.stats);
-  KeyPass a{lay.far.parts,
-            lay.far.tiles,
-            reinterpret_cast<float*>(base + 2 * lay.stats),
-            nlse2,
-            delta,
-            static_cast<__nv_bfloat16*>(dk),
-            static_cast<__nv_bfloat16*>(dv),
-            ld_dkv};
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  float* nlse2 = reinterpret_cast<float*>(base + kStatusBytes);
+  float* delta = reinterpret_cast<float*>(base + kStatusBytes + lay.stats);
+  SinkPlan* plan = reinterpret_cast<SinkPlan*>(base + lay.plan);
+  const KeyPass a{plan,
+                  reinterpret_cast<float*>(base + lay.part),
+                  nlse2,
+                  delta,
+                  static_cast<__nv_bfloat16*>(dk),
+                  static_cast<__nv_bfloat16*>(dv),
+                  ld_dkv};
   const Launch ctx{static_cast<cudaStream_t>(stream), static_cast<uint32_t*>(ws),
                    current_wait_budget_ns()};
   const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
@@ -1020,6 +1157,10 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
   st.d_o = static_cast<const __nv_bfloat16*>(d_o);
   st.ld_o = ld_o, st.ld_do = ld_do;
   st.lse = lse, st.nlse2 = nlse2, st.delta = delta;
+  st.plan = plan;
+  st.rec = reinterpret_cast<SlotRec*>(base + lay.rec);
+  st.before = reinterpret_cast<int64_t*>(base + lay.before);
+  st.ctas = lay.ctas;
   void* outs[3] = {dq, dk, dv};
   const int64_t lds[3] = {ld_dq, ld_dkv, ld_dkv};
   for (int i = 0; i < 3; ++i) {
@@ -1027,7 +1168,7 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
     st.ld_zero[i] = lds[i];
   }
   auto run = [&](auto dh) {
-    return launch_sink_grad<decltype(dh)::value>(ctx, dims, t, lay.far, a, st, sc,
+    return launch_sink_grad<decltype(dh)::value>(ctx, dims, t, a, lay.ctas, st, sc,
                                                  static_cast<__nv_bfloat16*>(dq), ld_dq);
   };
   const cudaError_t e = s.d == 128 ? run(std::integral_constant<int, 128>{})

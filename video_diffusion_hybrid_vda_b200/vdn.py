@@ -797,7 +797,7 @@ def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
         raise ValueError("rope: bf16, fp16 or fp32")
     xp, ld = _mat("x", x, rows, cols, dtype)
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=x.device)
+        out = x.new_empty((rows, cols))
     op, ld_out = _mat("out", out, rows, cols, dtype)
     pos, stride = _rope_positions(positions, plan, rows)
     _check(lib().vdn_rope(plan._ref, code, rows, H, xp, ld, pos, stride, 1 if inverse else 0, op,
@@ -829,9 +829,9 @@ def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rm
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
     rows, dtype, d = q.shape[0], q.dtype, plan.d
     if q_out is None:
-        q_out = torch.empty((rows, H * d), dtype=dtype, device=q.device)
+        q_out = q.new_empty((rows, H * d))
     if k_out is None:
-        k_out = torch.empty((rows, H_kv * d), dtype=dtype, device=q.device)
+        k_out = q.new_empty((rows, H_kv * d))
     _check(lib().vdn_qk_norm_rope(
         *args, *_mat("q_out", q_out, rows, H * d, dtype),
         *_mat("k_out", k_out, rows, H_kv * d, dtype), _raw_stream(stream, dev)),
@@ -847,17 +847,17 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
     has no norm.  dq may be dq_out and dk dk_out."""
     dev = _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
-    rows, dtype, d, device = q.shape[0], q.dtype, plan.d, q.device
+    rows, dtype, d = q.shape[0], q.dtype, plan.d
     if dq is None:
-        dq = torch.empty((rows, H * d), dtype=dtype, device=device)
+        dq = q.new_empty((rows, H * d))
     if dk is None:
-        dk = torch.empty((rows, H_kv * d), dtype=dtype, device=device)
+        dk = q.new_empty((rows, H_kv * d))
     if dwq is None and NORMS[q_norm]:
-        dwq = torch.empty(d, dtype=torch.float32, device=device)
+        dwq = q.new_empty(d, dtype=torch.float32)
     if dwk is None and NORMS[k_norm]:
-        dwk = torch.empty(d, dtype=torch.float32, device=device)
+        dwk = q.new_empty(d, dtype=torch.float32)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), device)
+        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), q.device)
     _check(lib().vdn_qk_norm_rope_backward(
         *args, *_mat("dq_out", dq_out, rows, H * d, dtype),
         *_mat("dk_out", dk_out, rows, H_kv * d, dtype), *_mat("dq", dq, rows, H * d, dtype),
@@ -924,7 +924,7 @@ def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=Non
     Lq = shape.Lq
     new = out is None
     if new:
-        out = torch.empty((Lq, H * d), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((Lq, H * d))
     if ws is None:
         ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(args[0])), q.device)
     _check(lib().vdn_sink_attn(
@@ -946,20 +946,20 @@ def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=
     are in a given one.  Returns (dq, dk, dv, ws)."""
     dev = _same_device(q, k, v, o, lse, d_o, cu_q, cu_k, dq, dk, dv, ws)
     shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
-    Lq, Lk, device, bf16 = shape.Lq, shape.Lk, q.device, torch.bfloat16
+    Lq, Lk, bf16 = shape.Lq, shape.Lk, torch.bfloat16
     new = (dq is None) | (dk is None) << 1 | (dv is None) << 2
     if dq is None:
-        dq = torch.empty((Lq, H * d), dtype=bf16, device=device)
+        dq = q.new_empty((Lq, H * d))
     if dk is None:
-        dk = torch.empty((Lk, H_kv * d), dtype=bf16, device=device)
+        dk = q.new_empty((Lk, H_kv * d))
     if dv is None:
-        dv = torch.empty((Lk, H_kv * d), dtype=bf16, device=device)
+        dv = q.new_empty((Lk, H_kv * d))
     dkp, ld_dkv = _mat("dk", dk, Lk, H_kv * d, bf16)
     dvp, ld_dv = _mat("dv", dv, Lk, H_kv * d, bf16)
     if ld_dv != ld_dkv:
         raise ValueError("dk and dv must share one row stride")
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), device)
+        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), q.device)
     _check(lib().vdn_sink_attn_backward(
         *args, *_mat("o", o, Lq, H * d, bf16), _lse_addr(lse, H, Lq),
         *_mat("d_o", d_o, Lq, H * d, bf16), *_mat("dq", dq, Lq, H * d, bf16), dkp, dvp, ld_dkv,
@@ -992,7 +992,7 @@ def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, win
             not positions.is_contiguous():
         raise ValueError("positions: contiguous int32 [B]")
     if out is None:
-        out = torch.empty((B, H * d), dtype=bf16, device=q.device)
+        out = q.new_empty((B, H * d))
     _check(lib().vdn_sink_attn_step(
         B, H, H_kv, d, window, sinks, *_mat("q", q, B, H * d, bf16), knp, vnp, ld_new,
         k_cache.data_ptr(), v_cache.data_ptr(), strides[1] if shape[1] > 1 else shape[2],
