@@ -74,10 +74,15 @@ struct StatsArgs {
 };
 
 // How the key pass's items are dealt out, written by one block of the
-// statistics launch.  Slot s (a key tile of a sequence) has weight[s] items a
-// key head (1 for keys that no query sees: they get zeros), the unit (s, hk)
-// covers [Hkv before[s] + hk weight[s], ...) of `total` items, and CTA c of
-// `ctas` the items [total c / ctas, total (c + 1) / ctas).
+// statistics launch.  Slot s (a key tile of a sequence) weighs its items of a
+// key head and kUnitCost more (loading the tile and storing its sums takes
+// about as long as that many items: 10 units and 56 items took 198 us where 1
+// and 56 took 136).  The unit (s, hk) covers [Hkv before[s] + hk weight[s], ...)
+// of `total`, its cost first, then its items; CTA c of `ctas` takes
+// [first[c], first[c + 1]), about total / ctas each, moved back to the unit's
+// begin where it would fall inside a unit's cost or before its first item.
+constexpr int kUnitCost = 3;
+
 struct SlotRec {
   int b, tile;     // sequence and its key tile
   int t0, tiles;   // query tiles (of 128) that see it
@@ -86,14 +91,11 @@ struct SlotRec {
 struct SinkPlan {
   int64_t total;
   int ctas;
-  int start[kCtas];    // slot of each CTA's first item
+  int start[kCtas];          // slot of each CTA's first item
+  int64_t first[kCtas + 1];
   SlotRec* rec;        // [slots]
   int64_t* before;     // [slots + 1]
 };
-
-__device__ __forceinline__ int64_t plan_first(int64_t total, int ctas, int c) {
-  return total / ctas * c + total % ctas * c / ctas;
-}
 
 __device__ __forceinline__ SlotRec key_slot(const SinkDims& s, int slot) {
   SlotRec r{0, -1, 0, 0};
@@ -128,7 +130,7 @@ __device__ void make_plan(const SinkDims& s, const StatsArgs& a) {
       r = key_slot(s, slot);
       a.rec[slot] = r;
     }
-    const int64_t w = r.tile < 0 ? 0 : max(1, r.tiles * group);
+    const int64_t w = r.tile < 0 ? 0 : r.tiles * group + kUnitCost;
     int64_t x = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -146,21 +148,21 @@ __device__ void make_plan(const SinkDims& s, const StatsArgs& a) {
   }
   const int64_t total = carry * s.Hkv;
   if (threadIdx.x == 0) a.before[slots] = carry;
-  // four items a CTA at least: loading a key tile and storing its sums costs
-  // about as much
-  int64_t n = total / 4;
+  // twice a unit's cost a CTA at least
+  int64_t n = total / (2 * kUnitCost);
   n = n < 1 ? 1 : n > a.ctas ? a.ctas : n;
   if (threadIdx.x == 0) {
     p->total = total;
     p->ctas = static_cast<int>(n);
     p->rec = a.rec;
     p->before = a.before;
+    p->first[n] = total;
   }
   __syncthreads();
   for (int c = threadIdx.x; c < n; c += 256) {
-    // the last slot that begins at or before the CTA's first item and is not
-    // empty: empty ones begin where the next begins
-    const int64_t x = plan_first(total, static_cast<int>(n), c);
+    int64_t x = total / n * c + total % n * c / n;
+    // the last slot that begins at or before x: empty ones begin where the
+    // next begins
     int lo = 0, hi = slots;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -169,10 +171,13 @@ __device__ void make_plan(const SinkDims& s, const StatsArgs& a) {
       else
         hi = mid;
     }
+    const int64_t begin = a.before[lo] * s.Hkv, weight = a.before[lo + 1] - a.before[lo];
+    const int64_t in = weight > 0 ? (x - begin) % weight : 0;
+    if (in <= kUnitCost) x -= in;
     p->start[c] = lo;
+    p->first[c] = x;
   }
 }
-
 constexpr int kStatsRows = 8;
 
 __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, const StatsArgs a) {
@@ -279,11 +284,11 @@ struct KeyCursor {
   int64_t x, x1;   // next item and end
   int slot, hk;
   SlotRec r;
-  int weight, i0, i1;
+  int weight, i0, i1;  // items [i0, i1)
   bool whole;
   __device__ void init(const SinkPlan* p, int c) {
-    x = plan_first(p->total, p->ctas, c);
-    x1 = plan_first(p->total, p->ctas, c + 1);
+    x = p->first[c];
+    x1 = p->first[c + 1];
     slot = p->start[c] - 1;
     hk = 0;
     weight = 0;
@@ -298,17 +303,17 @@ struct KeyCursor {
         ++slot;
         r = p->rec[slot];
       } while (r.tile < 0);
-      weight = max(1, r.tiles * (s.H / s.Hkv));
+      weight = r.tiles * (s.H / s.Hkv) + kUnitCost;
       hk = first ? static_cast<int>((x - p->before[slot] * s.Hkv) / weight) : 0;
     } else {
       ++hk;
     }
     const int64_t begin = p->before[slot] * s.Hkv + static_cast<int64_t>(hk) * weight;
-    i0 = static_cast<int>(x - begin);
-    i1 = static_cast<int>(min(static_cast<int64_t>(weight), x1 - begin));
-    whole = i0 == 0 && i1 == weight;
-    x = begin + i1;
-    if (r.tiles == 0) i1 = i0;  // a unit that no query sees
+    const int end = static_cast<int>(min(static_cast<int64_t>(weight), x1 - begin));
+    i0 = max(0, static_cast<int>(x - begin) - kUnitCost);
+    i1 = end - kUnitCost;
+    whole = i0 == 0 && end == weight;
+    x = begin + end;
     return true;
   }
 };
@@ -340,7 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* ds_ready = p_ready + kGroups;       // [kGroups]
   uint64_t* acc_full = ds_ready + kGroups;      // a unit's sums are complete
   uint64_t* acc_free = acc_full + 1;            // and have been read
-  uint64_t* mma_done = acc_free + 1;
+  uint64_t* kv_free = acc_free + 1;             // a unit's scores are all formed
+  uint64_t* mma_done = kv_free + 1;
   uint64_t* cut = mma_done + 1;                 // tiles whose last rows are zeroed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut + 1);
 
@@ -369,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_free, kGroups * 128);
+    mbar_init(kv_free, 1);
     mbar_init(mma_done, 1);
     mbar_init(cut, 1);
     fence_mbar_init();
@@ -396,14 +403,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ================================================================ TMA
     const bool leader = lane_id() == 0;
-    int n = 0, t = 0, cuts = 0;  // units, items and cut tiles so far
+    int n = 0, t = 0, cuts = 0;  // units with items, items and cut tiles so far
     bool ok = true;
     while (ok && cur.next(dims, a.plan)) {
+      if (cur.i0 >= cur.i1) continue;
       const SinkSeq seq = sink_seq(dims, cur.r.b);
       const int q_base = sink_slot_base(dims.cu_q, cur.r.b, dims.Lq, 128);
       const int key0 = seq.k0 + 128 * cur.r.tile;
-      // the last unit's products have read K and V
-      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(acc_full, (n - 1) & 1, budget_ns))) {
+      // K and V are free once the last item's scores are formed, while its
+      // sums are still to come
+      if (n > 0 && !__all_sync(0xffffffffu, mbar_wait(kv_free, (n - 1) & 1, budget_ns))) {
         ok = false;
         break;
       }
@@ -511,13 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return true;
       };
-      int n = 0, t = 0;
+      int n = 0, loads = 0, t = 0;
       bool ok = true;
       while (ok && cur.next(dims, a.plan)) {
         const int items = cur.i1 - cur.i0;
-        if (!(ok = mbar_wait(kv_full, n & 1, budget_ns))) break;
-        tc_fence_after();
-        if (items > 0 && !(ok = scores(t) && d_scores(t))) break;
+        if (items > 0) {
+          if (!(ok = mbar_wait(kv_full, loads++ & 1, budget_ns))) break;
+          tc_fence_after();
+          if (!(ok = scores(t) && d_scores(t))) break;
+          if (items == 1) umma_commit(kv_free);
+        }
         // the last unit's sums have been read
         if (n > 0 && !(ok = mbar_wait(acc_free, (n - 1) & 1, budget_ns))) break;
         tc_fence_after();
@@ -531,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = sums(ds_ready, dk_addr, tmem + 128, q_tile(t), t, i > 0))) break;
           umma_commit(&q_empty[t % Cfg::STAGES]);
           if (more && !(ok = d_scores(t + 1))) break;
+          if (i + 2 == items) umma_commit(kv_free);
         }
         if (!ok) break;
         umma_commit(acc_full);
@@ -703,14 +716,18 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, con
   const int slot = blockIdx.x / dims.Hkv, hk = blockIdx.x % dims.Hkv;
   const SlotRec r = p->rec[slot];
   if (r.tile < 0) return;
-  const int64_t weight = max(1, r.tiles * (dims.H / dims.Hkv));
+  const int64_t weight = r.tiles * (dims.H / dims.Hkv) + kUnitCost;
   const int64_t begin = p->before[slot] * dims.Hkv + hk * weight, last = begin + weight - 1;
-  auto owner = [&](int64_t x) {  // the CTA of item x
-    int c = static_cast<int>(static_cast<double>(x) * p->ctas / static_cast<double>(p->total));
-    c = min(c, p->ctas - 1);
-    while (c > 0 && plan_first(p->total, p->ctas, c) > x) --c;
-    while (c + 1 < p->ctas && plan_first(p->total, p->ctas, c + 1) <= x) ++c;
-    return c;
+  auto owner = [&](int64_t x) {  // the last CTA that begins at or before x
+    int lo = 0, hi = p->ctas;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p->first[mid] <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
   };
   const int first = owner(begin), end = owner(last);
   if (first == end) return;
@@ -929,6 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + row;
     const float nl = nlse2[at], dl = delta[at];
     const float scale_log2 = scale * 1.4426950408889634f;
+    const uint64_t cc = f32x2_pack(scale_log2, scale_log2), nl2 = f32x2_pack(nl, nl);
     const SinkMask m = dims.m;
     bool ok = true;
     for (int j = 0; j < kt.n; ++j) {
@@ -948,8 +966,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(s_free);
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        x[c] = __float_as_uint(exp2_mufu(fmaf(__uint_as_float(x[c]), scale_log2, nl)));
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t y =
+            f32x2_fma((static_cast<uint64_t>(x[2 * e + 1]) << 32) | x[2 * e], cc, nl2);
+        x[2 * e] = __float_as_uint(exp2_mufu(f32x2_lo(y)));
+        x[2 * e + 1] = __float_as_uint(exp2_mufu(f32x2_hi(y)));
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&dp_full[j & 1], (j >> 1) & 1, budget_ns))) {
         ok = false;
         break;
@@ -1036,9 +1058,10 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 GradLayout grad_layout(const vdn_sink_shape& s) {
   GradLayout l;
   const size_t k_slots = sink_slots(s.Lk, s.B, 128);
-  // no more CTAs than four items each could make: a tile has at most
-  // (Lq + 127) / 128 + 1 query tiles of each of its heads
-  const double items = static_cast<double>(k_slots) * s.H * (s.Lq / 128 + 2) / 4;
+  // no more CTAs than the plan could give twice a unit's cost: a tile has at
+  // most Lq / 128 + 2 query tiles of each of its heads
+  const double items = static_cast<double>(k_slots) * s.H *
+                       (s.Lq / 128 + 2 + kUnitCost) / (2 * kUnitCost);
   l.ctas = items < 1 ? 1 : items > kCtas ? kCtas : static_cast<int>(items);
   l.stats = align256(static_cast<size_t>(s.H) * sink_slots(s.Lq, s.B, 128) * 128 * sizeof(float));
   l.plan = kStatusBytes + 2 * l.stats;
