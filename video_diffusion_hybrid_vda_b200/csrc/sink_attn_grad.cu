@@ -53,7 +53,7 @@ struct GradCfg {
 };
 
 // Per query, in tiles of 128 (the slots of sink_attn.cuh): -lse log2 e and
-// D = dO . o.  Rows past the sequence's end get -inf and 0: P = 0 there.
+// -D = -dO . o.  Rows past the sequence's end get -inf and 0: P = 0 there.
 // Rows of dq, dk and dv of no sequence are zeroed where asked.
 // A block takes 8 rows of a slot, DH / 8 lanes a (row, head), four at a time
 // in flight: reading o and dO once is the whole cost.
@@ -64,7 +64,7 @@ struct StatsArgs {
   int64_t ld_o, ld_do;
   const float* lse;
   float* nlse2;
-  float* delta;
+  float* ndelta;
   void* zero[3];       // dq, dk, dv or null
   int64_t ld_zero[3];
   struct SinkPlan* plan;
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
             on[n] ? a.lse[static_cast<int64_t>(h) * dims.Lq + tile0 + first + i] : -INFINITY;
         const bool none = v == -INFINITY;
         a.nlse2[at] = none ? -INFINITY : -v * 1.4426950408889634f;
-        a.delta[at] = none ? 0.f : t;
+        a.ndelta[at] = none ? 0.f : -t;
       }
     }
   }
@@ -271,9 +271,9 @@ __device__ __forceinline__ void grad_mma_scores(uint32_t d, uint32_t a_tile, uin
 
 struct KeyPass {
   const SinkPlan* plan;
-  float* part;        // [ctas][2][dV, dK][DH][128]: a CTA's first and last tile where shared
+  float* part;        // [ctas][2][dV, dK][128][DH]: a CTA's first and last tile where shared
   const float* nlse2;
-  const float* delta;
+  const float* ndelta;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
   int64_t ld;
@@ -426,10 +426,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++n;
-      for (int i = cur.i0; i < cur.i1; ++i) {
+      int qi = cur.i0 % cur.r.tiles, h = cur.hk * group + cur.i0 / cur.r.tiles;
+      for (int i = cur.i0; i < cur.i1; ++i, h += qi + 1 == cur.r.tiles,
+               qi = qi + 1 == cur.r.tiles ? 0 : qi + 1) {
         const int s = t % Cfg::STAGES;
         const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
-        const int qt = cur.r.t0 + i % cur.r.tiles, h = cur.hk * group + i / cur.r.tiles;
+        const int qt = cur.r.t0 + qi;
         const int row = seq.q0 + 128 * qt, valid = min(128, seq.nq() - 128 * qt);
         uint8_t* qb = ring + s * 2 * Cfg::TILE;
         uint8_t* dob = qb + Cfg::TILE;
@@ -443,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(&st_full[s], Cfg::STATS);
           const int64_t at = (static_cast<int64_t>(h) * q_slots + q_base + qt) * 128;
           bulk_load(stats + s * Cfg::STATS, a.nlse2 + at, 512, &st_full[s]);
-          bulk_load(stats + s * Cfg::STATS + 512, a.delta + at, 512, &st_full[s]);
+          bulk_load(stats + s * Cfg::STATS + 512, a.ndelta + at, 512, &st_full[s]);
           mbar_arrive_expect_tx(qbar, (valid < 128 ? 2 : 1) * Cfg::TILE);
           for (int sl = 0; sl < Cfg::SLABS; ++sl)
             tma_load_2d(qb + sl * 16384, &qmap, qbar, h * DH + 64 * sl, row);
@@ -567,13 +569,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (ok && cur.next(dims, a.plan)) {
       const SinkSeq seq = sink_seq(dims, cur.r.b);
       const int ks = 128 * cur.r.tile, kw = ks + quarter * 32, key = kw + lane_id();
+      // position of this part's first query, of the unit's first query tile
+      // and of the item's
+      const int p_first = 128 * cur.r.t0 + seq.shift() + 32 * w;
+      int qi = cur.r.tiles > 0 ? cur.i0 % cur.r.tiles : 0;
       for (int i = cur.i0; i < cur.i1; ++i, ++t) {
         const int s = t % Cfg::STAGES;
-        // position of this part's first query
-        const int p0 = 128 * (cur.r.t0 + i % cur.r.tiles) + seq.shift() + 32 * w;
+        const int p0 = p_first + 128 * qi;
+        if (++qi == cur.r.tiles) qi = 0;
         const bool edge = !sink_sees_all(m, p0, p0 + 31, kw, kw + 31);
-        const uint32_t see = sink_bits(key - m.ahead - p0,
-                                       key < m.sinks ? 32 : key - p0 + m.window, 0);
         if (!__all_sync(0xffffffffu,
                         mbar_wait(&st_full[s], (t / Cfg::STAGES) & 1, budget_ns) &&
                             mbar_wait(s_full, t & 1, budget_ns))) {
@@ -601,7 +605,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             x[c + 1] = __float_as_uint(exp2_mufu(f32x2_hi(y)));
           }
         }
+        uint32_t see = 0xffffffffu;
         if (edge) {
+          see = sink_bits(key - m.ahead - p0, key < m.sinks ? 32 : key - p0 + m.window, 0);
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = see & (1u << c) ? x[c] : 0;
         }
@@ -631,11 +637,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const ulonglong2 d2 = dl[e];
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
-            const uint64_t d = f ? d2.y : d2.x;
             const int c = 4 * e + 2 * f;
-            pk[2 * e + f] = pack_bf16x2(
-                __uint_as_float(x[c]) * (__uint_as_float(g[c]) - f32x2_lo(d)),
-                __uint_as_float(x[c + 1]) * (__uint_as_float(g[c + 1]) - f32x2_hi(d)));
+            const uint64_t y = f32x2_mul(
+                (static_cast<uint64_t>(x[c + 1]) << 32) | x[c],
+                f32x2_add((static_cast<uint64_t>(g[c + 1]) << 32) | g[c], f ? d2.y : d2.x));
+            pk[2 * e + f] = pack_bf16x2(f32x2_lo(y), f32x2_hi(y));
           }
         }
         tmem_st16(dp_addr, pk);
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            cur.hk * DH + c0;
       float* part = a.part +
                     ((static_cast<int64_t>(cta) * 2 + (cur.i0 == 0)) * 2 + which) * (DH * 128) +
-                    c0 * 128 + row;
+                    row * DH + c0;
 #pragma unroll 1
       for (int c = 0; c < DH / 2; c += 32) {
         uint32_t x[32];
@@ -677,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!cur.whole) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(c + e) * 128] = __uint_as_float(x[e]);
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + c + e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         } else if (live) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // dK and dV of the units that several CTAs share: the sum of their parts, the
-// CTA with the unit's first items first.  A block: 32 columns of one of them.
+// CTA with the unit's first items first.
 template <int DH>
 __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, const KeyPass a,
                                                         float scale) {
@@ -732,29 +739,28 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, con
   const int first = owner(begin), end = owner(last);
   if (first == end) return;
   const SinkSeq seq = sink_seq(dims, r.b);
-  constexpr int BLOCKS = DH / 32;
-  const int which = blockIdx.y / BLOCKS, c0 = blockIdx.y % BLOCKS * 32;
-  const int row = threadIdx.x & 127, c1 = c0 + (threadIdx.x >> 7) * 16;
-  float x[16] = {};
+  // blockIdx.y: dV or dK, and 16 of the 128 keys; a thread: 8 columns of a key
+  const int which = blockIdx.y >> 3;
+  const int row = (blockIdx.y & 7) * 16 + threadIdx.x / (DH / 8), c0 = threadIdx.x % (DH / 8) * 8;
+  if (threadIdx.x >= 16 * (DH / 8) || 128 * r.tile + row >= seq.nk()) return;
+  float x[8] = {};
   for (int c = first; c <= end; ++c) {
-    const float* in = a.part + ((static_cast<int64_t>(c) * 2 + (c == first)) * 2 + which) *
-                                   (DH * 128) + c1 * 128 + row;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] += in[e * 128];
+    const float4* in = reinterpret_cast<const float4*>(
+        a.part + ((static_cast<int64_t>(c) * 2 + (c == first)) * 2 + which) * (DH * 128) +
+        row * DH + c0);
+    const float4 u = in[0], v = in[1];
+    x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
+    x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
   }
-  if (128 * r.tile + row >= seq.nk()) return;
   const float f = which ? scale : 1.f;
   __nv_bfloat16* dst = (which ? a.dk : a.dv) +
-                       static_cast<int64_t>(seq.k0 + 128 * r.tile + row) * a.ld + hk * DH + c1;
-#pragma unroll
-  for (int e = 0; e < 16; e += 8) {
-    uint4 u;
-    u.x = pack_bf16x2(x[e] * f, x[e + 1] * f);
-    u.y = pack_bf16x2(x[e + 2] * f, x[e + 3] * f);
-    u.z = pack_bf16x2(x[e + 4] * f, x[e + 5] * f);
-    u.w = pack_bf16x2(x[e + 6] * f, x[e + 7] * f);
-    *reinterpret_cast<uint4*>(dst + e) = u;
-  }
+                       static_cast<int64_t>(seq.k0 + 128 * r.tile + row) * a.ld + hk * DH + c0;
+  uint4 u;
+  u.x = pack_bf16x2(x[0] * f, x[1] * f);
+  u.y = pack_bf16x2(x[2] * f, x[3] * f);
+  u.z = pack_bf16x2(x[4] * f, x[5] * f);
+  u.w = pack_bf16x2(x[6] * f, x[7] * f);
+  *reinterpret_cast<uint4*>(dst) = u;
 }
 
 // ---------------------------------------------------------------- query pass
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                            const __grid_constant__ CUtensorMap domap,
                            const __grid_constant__ CUtensorMap kmap,
                            const __grid_constant__ CUtensorMap vmap, const SinkDims dims,
-                           const float* __restrict__ nlse2, const float* __restrict__ delta,
+                           const float* __restrict__ nlse2, const float* __restrict__ ndelta,
                            float scale, __nv_bfloat16* __restrict__ dq, int64_t ld_dq,
                            uint32_t* status, uint64_t budget_ns) {
   using Cfg = GradCfg<DH>;
@@ -944,16 +950,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = quarter * 32 + lane_id();
     const int p = pa + row, pw = pa + quarter * 32;
     const int64_t at = (static_cast<int64_t>(h) * slots + slot) * 128 + row;
-    const float nl = nlse2[at], dl = delta[at];
+    const float nl = nlse2[at], nd = ndelta[at];
     const float scale_log2 = scale * 1.4426950408889634f;
-    const uint64_t cc = f32x2_pack(scale_log2, scale_log2), nl2 = f32x2_pack(nl, nl);
+    const uint64_t cc = f32x2_pack(scale_log2, scale_log2), nl2 = f32x2_pack(nl, nl),
+                   nd2 = f32x2_pack(nd, nd);
     const SinkMask m = dims.m;
     bool ok = true;
     for (int j = 0; j < kt.n; ++j) {
       const int ks = kt.start(j) + 32 * w, valid = kt.valid(j) - 32 * w;
       const bool edge = valid < 32 || !sink_sees_all(m, pw, pw + 31, ks, ks + 31);
-      const uint32_t see = sink_bits(p - m.window + 1 - ks, min(valid, p + m.ahead + 1 - ks),
-                                     m.sinks - ks);
       if (!__all_sync(0xffffffffu, mbar_wait(s_full, j & 1, budget_ns))) {
         ok = false;
         break;
@@ -982,17 +987,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(g_addr, g);
       tmem_ld_wait();
       reg_fence(g);
+      if (edge) {  // of a hidden pair P is not 0 here, and dP may be NaN
+        const uint32_t see = sink_bits(p - m.window + 1 - ks, min(valid, p + m.ahead + 1 - ks),
+                                       m.sinks - ks);
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        g[c] = __float_as_uint(__uint_as_float(x[c]) * (__uint_as_float(g[c]) - dl));
-      if (edge) {
-#pragma unroll
-        for (int c = 0; c < 32; ++c) g[c] = see & (1u << c) ? g[c] : 0;
+        for (int c = 0; c < 32; ++c) {
+          x[c] = see & (1u << c) ? x[c] : 0;
+          g[c] = see & (1u << c) ? g[c] : 0;
+        }
       }
       uint32_t ds[16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        ds[e] = pack_bf16x2(__uint_as_float(g[2 * e]), __uint_as_float(g[2 * e + 1]));
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t y = f32x2_mul(
+            (static_cast<uint64_t>(x[2 * e + 1]) << 32) | x[2 * e],
+            f32x2_add((static_cast<uint64_t>(g[2 * e + 1]) << 32) | g[2 * e], nd2));
+        ds[e] = pack_bf16x2(f32x2_lo(y), f32x2_hi(y));
+      }
       tmem_st16(g_addr, ds);
       tmem_st_wait();
       tc_fence_before();
@@ -1091,13 +1102,13 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
     sink_key_pass_kernel<DH><<<ctas, kThreads, Cfg::SMEM, ctx.stream>>>(
         t.q, t.d_o, t.k, t.v, dims, a, scale, ctx.status, ctx.budget_ns);
     if (cudaError_t e = cudaGetLastError()) return e;
-    sink_join_kernel<DH><<<dim3(sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, DH / 16), 256, 0,
+    sink_join_kernel<DH><<<dim3(sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, 16), 256, 0,
                            ctx.stream>>>(dims, a, scale);
     if (cudaError_t e = cudaGetLastError()) return e;
   }
   if (dims.Lq > 0)
     sink_query_pass_kernel<DH><<<q_slots * dims.H, kThreads, Cfg::SMEM, ctx.stream>>>(
-        t.q, t.d_o, t.k, t.v, dims, a.nlse2, a.delta, scale, dq, ld_dq, ctx.status,
+        t.q, t.d_o, t.k, t.v, dims, a.nlse2, a.ndelta, scale, dq, ld_dq, ctx.status,
         ctx.budget_ns);
   return cudaGetLastError();
 }
@@ -1162,12 +1173,12 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
   if (s.Lk == 0) t.k = t.v = t.q;
   uint8_t* base = static_cast<uint8_t*>(ws);
   float* nlse2 = reinterpret_cast<float*>(base + kStatusBytes);
-  float* delta = reinterpret_cast<float*>(base + kStatusBytes + lay.stats);
+  float* ndelta = reinterpret_cast<float*>(base + kStatusBytes + lay.stats);
   SinkPlan* plan = reinterpret_cast<SinkPlan*>(base + lay.plan);
   const KeyPass a{plan,
                   reinterpret_cast<float*>(base + lay.part),
                   nlse2,
-                  delta,
+                  ndelta,
                   static_cast<__nv_bfloat16*>(dk),
                   static_cast<__nv_bfloat16*>(dv),
                   ld_dkv};
@@ -1179,7 +1190,7 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
   st.o = static_cast<const __nv_bfloat16*>(o);
   st.d_o = static_cast<const __nv_bfloat16*>(d_o);
   st.ld_o = ld_o, st.ld_do = ld_do;
-  st.lse = lse, st.nlse2 = nlse2, st.delta = delta;
+  st.lse = lse, st.nlse2 = nlse2, st.ndelta = ndelta;
   st.plan = plan;
   st.rec = reinterpret_cast<SlotRec*>(base + lay.rec);
   st.before = reinterpret_cast<int64_t*>(base + lay.before);
