@@ -85,6 +85,14 @@ CASES = [  # lens_q, lens_k, H, Hkv, d, window, sinks, ahead, pad
     ([3, 2], [4100, 77], 2, 1, 64, 2000, 4, 0, 8),
     ([300], [4000], 1, 1, 64, 1 << 30, 0, 0, 0),
     ([2600], [2600], 8, 2, 128, 513, 4, 0, 0),
+    ([9], [2000], 8, 1, 64, 700, 4, 0, 0),              # heads that share a unit's rows
+    ([1], [300], 32, 1, 128, 1 << 30, 0, 0, 8),
+    ([16, 3, 30], [16, 500, 200], 16, 2, 128, 40, 3, 2, 0),
+    ([100, 20], [100, 300], 6, 3, 64, 50, 2, 0, 0),
+    ([0, 64, 0], [5, 64, 0], 4, 1, 128, 64, 0, 10, 0),
+    # several units a CTA, some of whose row tiles take no keys
+    ([257, 130, 1, 64, 300, 513] * 7, [257, 130, 1, 64, 300, 513] * 7, 8, 4, 64, 100, 4, 0, 0),
+    ([257, 20, 384] * 12, [0, 500, 384] * 12, 6, 6, 128, 70, 2, 0, 0),
 ]
 
 
