@@ -9,13 +9,13 @@
 // 256 rows (two 128-row tiles) of one sequence and key head: 256 queries of a
 // head, or, where sequences are short and heads share a key head, fewer
 // queries of several heads, so that a key tile is loaded and multiplied once
-// for all of them.  A unit walks the keys its queries see between them in
-// tiles of 128; a row tile leaves out the key tiles it does not touch (the
-// window's two ends), and only key tiles that cross the mask's edge pay for
-// comparisons.  One CTA an SM takes units in turn, heaviest first; its roles
-// run ahead of each other, so the next unit's loads and scores begin while
-// the last one's output is stored (one CTA a unit: 95 us instead of XX for
-// 8097 tokens, 16 heads, window 1024).
+// for all of them.  A CTA takes a unit, heaviest first, and walks the keys its
+// queries see between them in tiles of 128; a row tile leaves out the key
+// tiles it does not touch (the window's two ends), and only key tiles that
+// cross the mask's edge pay for comparisons.  (Persistent CTAs that begin the
+// next unit's loads and scores while the last output is stored were not
+// faster: 8097 tokens, 16 heads, window 1024 took 122 us with units dealt out
+// in turn against 104 us with one CTA a unit, 16384 tokens the same.)
 //   warp 0      TMA: Q, then K and V tiles through a ring; rows of a V tile
 //               past its interval are zeroed before the tile is handed on
 //   warp 1      tcgen05.mma: S_i = Q_i K^T, O_i += P_i V (P_i from TMEM)
@@ -60,45 +60,34 @@ struct SinkCut {
   int rows, splits;
 };
 
-// A CTA's walk over its units; every role keeps its own.
-struct SinkCursor {
-  int64_t u, total, step;
+struct SinkUnit {
   int row0, row1;     // query rows of the unit and the end of its sequence
   int h0, hk, split;  // first head, key head
   int pa, pb;         // positions of its first and last query
   int k0, j0, j1;     // first key row of the sequence; key tiles [j0, j1)
   SinkKeyTiles kt;
-  __device__ void init(const SinkDims& s, const SinkCut& c) {
-    u = blockIdx.x;
-    step = gridDim.x;
-    total = static_cast<int64_t>(sink_slots(s.Lq, s.B, c.rows)) * (s.H * c.rows / 256) * c.splits;
-  }
-  // The next unit that has queries; false at the end.
-  __device__ bool next(const SinkDims& s, const SinkCut& c) {
+  // The CTA's unit; false if it has no queries.
+  __device__ bool init(const SinkDims& s, const SinkCut& c) {
     const int per_slot = s.H * c.rows / 256 * c.splits;
-    while (u < total) {
-      // heaviest first: the last queries of a sequence see the most keys
-      const int slot = sink_slots(s.Lq, s.B, c.rows) - 1 - static_cast<int>(u / per_slot);
-      const int in = static_cast<int>(u % per_slot);
-      u += step;
-      const int b = sink_slot_seq(s.cu_q, s.B, s.Lq, c.rows, slot);
-      const SinkSeq seq = sink_seq(s, b);
-      const int at = c.rows * (slot - sink_slot_base(s.cu_q, b, s.Lq, c.rows));
-      if (at >= seq.nq()) continue;
-      row0 = seq.q0 + at;
-      row1 = seq.q1;
-      h0 = in / c.splits * (256 / c.rows);
-      split = in % c.splits;
-      hk = h0 / (s.H / s.Hkv);
-      pa = at + seq.shift();
-      pb = min(pa + c.rows - 1, seq.nk() - 1);
-      k0 = seq.k0;
-      kt.init(s.m, pa, pb, seq.nk());
-      j0 = static_cast<int>(static_cast<int64_t>(kt.n) * split / c.splits);
-      j1 = static_cast<int>(static_cast<int64_t>(kt.n) * (split + 1) / c.splits);
-      return true;
-    }
-    return false;
+    // heaviest first: the last queries of a sequence see the most keys
+    const int slot = sink_slots(s.Lq, s.B, c.rows) - 1 - static_cast<int>(blockIdx.x) / per_slot;
+    const int in = static_cast<int>(blockIdx.x) % per_slot;
+    const int b = sink_slot_seq(s.cu_q, s.B, s.Lq, c.rows, slot);
+    const SinkSeq seq = sink_seq(s, b);
+    const int at = c.rows * (slot - sink_slot_base(s.cu_q, b, s.Lq, c.rows));
+    if (at >= seq.nq()) return false;
+    row0 = seq.q0 + at;
+    row1 = seq.q1;
+    h0 = in / c.splits * (256 / c.rows);
+    split = in % c.splits;
+    hk = h0 / (s.H / s.Hkv);
+    pa = at + seq.shift();
+    pb = min(pa + c.rows - 1, seq.nk() - 1);
+    k0 = seq.k0;
+    kt.init(s.m, pa, pb, seq.nk());
+    j0 = static_cast<int>(static_cast<int64_t>(kt.n) * split / c.splits);
+    j1 = static_cast<int>(static_cast<int64_t>(kt.n) * (split + 1) / c.splits);
+    return true;
   }
   // Positions of row tile i (none: last < first).
   __device__ int first(const SinkCut& c, int i) const { return c.rows == 256 ? pa + 128 * i : pa; }
@@ -112,14 +101,14 @@ struct SinkCursor {
   }
 };
 
-// Softmax of one 128-row tile of each unit: one thread per row.
+// Softmax of one 128-row tile of the unit: one thread per row.
 template <int DH>
-__device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, SinkCursor& cur,
+__device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, const SinkUnit& cur,
                                              const SinkDims& dims, const SinkCut& cut,
                                              uint64_t* s_full, uint64_t* o_done, uint64_t* p_half,
-                                             uint64_t* p_ready, uint64_t* o_free,
-                                             float scale_log2, const SinkOut& out,
-                                             uint32_t* status, uint64_t budget_ns) {
+                                             uint64_t* p_ready, float scale_log2,
+                                             const SinkOut& out, uint32_t* status,
+                                             uint64_t budget_ns) {
   const uint32_t quarter = warp_id() & 3;
   const int row = quarter * 32 + lane_id();
   const uint32_t lane_off = (quarter * 32) << 16;
@@ -130,171 +119,164 @@ __device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, SinkCursor& c
   const int query = (128 * i + row) & (cut.rows - 1), head = (128 * i + row) / cut.rows;
   const int wq = (128 * i + quarter * 32) & (cut.rows - 1);
   const int warp_queries = min(32, cut.rows);
-  int n = 0;  // key tiles taken so far, of all units
-  while (cur.next(dims, cut)) {
-    const int p = cur.pa + query, pw = cur.pa + wq;
-    float m_used = -INFINITY;  // running maximum, log2 domain (scaled)
-    float l = 0.f;
-    const int n0 = n;
-    for (int j = cur.j0; j < cur.j1; ++j) {
-      if (!cur.takes(dims, cut, i, j)) continue;
-      const int ks = cur.kt.start(j);
-      const int valid = cur.kt.valid(j);
-      const bool edge = valid < 128 || !sink_sees_all(m, pw, pw + warp_queries - 1, ks, ks + 127);
-      // warp-uniform decision: tcgen05.ld/st below are warp-collective
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_full[i], n & 1, budget_ns))) return false;
-      tc_fence_after();
-      uint32_t sr[128];
-      uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
-      uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
-      uint32_t (&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
-      uint32_t (&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
-      auto hide = [&](int c0) {  // of columns [c0, c0 + 64), those that are not visible
-#pragma unroll
-        for (int w = c0; w < c0 + 64; w += 32) {
-          const uint32_t see = sink_bits(p - m.window + 1 - ks - w,
-                                         min(valid, p + m.ahead + 1 - ks) - w, m.sinks - ks - w);
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            sr[w + c] = see & (1u << c) ? sr[w + c] : __float_as_uint(-INFINITY);
-        }
-      };
-      tmem_ld32(s_addr, s0);
-      tmem_ld32(s_addr + 32, s1);
-      tmem_ld_wait();
-      reg_fence(s0);
-      reg_fence(s1);
-      tmem_ld32(s_addr + 64, s2);
-      tmem_ld32(s_addr + 96, s3);
-      if (edge) hide(0);
-      auto sv = [&](int c) { return __uint_as_float(sr[c]); };
-      float mx8[8];
-#pragma unroll
-      for (int a = 0; a < 8; ++a) mx8[a] = fmax3(sv(a), sv(a + 8), sv(a + 16));
-#pragma unroll
-      for (int c = 24; c < 56; c += 16)
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
-#pragma unroll
-      for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], sv(56 + a));
-      tmem_ld_wait();
-      reg_fence(s2);
-      reg_fence(s3);
-      if (edge) hide(64);
-#pragma unroll
-      for (int c = 64; c < 128; c += 16)
-#pragma unroll
-        for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
-      const float mt = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
-                             fmaxf(mx8[6], mx8[7])) *
-                       scale_log2;
-      // The maximum in use moves only when some row's grew by more than 2^8
-      // (then P stays below 2^8 and O is not rescaled for nothing).  A row
-      // that has seen no key keeps -inf: its factor is 0 and its P below
-      // takes 0.
-      if (__any_sync(0xffffffffu, mt > m_used + 8.f)) {
-        const float m_new = fmaxf(m_used, mt);
-        const float factor = m_used == -INFINITY ? 0.f : exp2_mufu(m_used - m_new);
-        l *= factor;
-        if (n > n0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)))
-            return false;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < DH; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c, o);
-            tmem_ld_wait();
-            reg_fence(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-            tmem_st32(o_addr + c, o);
-          }
-        }
-        m_used = m_new;
-      }
-      const float m_sub = m_used == -INFINITY ? 0.f : m_used;
-      const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
-      const uint64_t nm = f32x2_pack(-m_sub, -m_sub);
-      uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint64_t xs = f32x2_fma(
-              (static_cast<uint64_t>(sr[32 * q + 2 * e + 1]) << 32) | sr[32 * q + 2 * e], cc, nm);
-          const uint64_t pp = f32x2_pack(exp2_mufu(f32x2_lo(xs)), exp2_mufu(f32x2_hi(xs)));
-          acc2[e & 3] = f32x2_add(acc2[e & 3], pp);
-          pk[e] = pack_bf16x2(f32x2_lo(pp), f32x2_hi(pp));
-        }
-        tmem_st16(s_addr + 16 * q, pk);
-        if (q == 1) {  // the product over the first 64 keys starts now
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_half[i]);
-        }
-      }
-      acc2[0] = f32x2_add(f32x2_add(acc2[0], acc2[1]), f32x2_add(acc2[2], acc2[3]));
-      l += f32x2_lo(acc2[0]) + f32x2_hi(acc2[0]);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&p_ready[i]);
-      ++n;
-    }
-    // ---------------------------------------------------------- the unit's output
-    const bool any = n > n0;
-    if (any && !__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)))
-      return false;
+  const int p = cur.pa + query, pw = cur.pa + wq;
+  float m_used = -INFINITY;  // running maximum, log2 domain (scaled)
+  float l = 0.f;
+  int n = 0;                 // key tiles taken so far
+  for (int j = cur.j0; j < cur.j1; ++j) {
+    if (!cur.takes(dims, cut, i, j)) continue;
+    const int ks = cur.kt.start(j);
+    const int valid = cur.kt.valid(j);
+    const bool edge = valid < 128 || !sink_sees_all(m, pw, pw + warp_queries - 1, ks, ks + 127);
+    // warp-uniform decision: tcgen05.ld/st below are warp-collective
+    if (!__all_sync(0xffffffffu, mbar_wait(&s_full[i], n & 1, budget_ns))) return false;
     tc_fence_after();
-    const int r = cur.row0 + query, h = cur.h0 + head;
-    const bool live = r < cur.row1 && in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH,
-                                                DH, static_cast<int64_t>(dims.H) * DH);
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: o = 0
-    __nv_bfloat16* dst = out.o + static_cast<int64_t>(r) * out.ld_o + h * DH;
-    float* part = out.part_o + ((static_cast<int64_t>(cur.split) * dims.Lq + r) * dims.H + h) * DH;
+    uint32_t sr[128];
+    uint32_t (&s0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+    uint32_t (&s1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+    uint32_t (&s2)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[64]);
+    uint32_t (&s3)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[96]);
+    auto hide = [&](int c0) {  // of columns [c0, c0 + 64), those that are not visible
+#pragma unroll
+      for (int w = c0; w < c0 + 64; w += 32) {
+        const uint32_t see = sink_bits(p - m.window + 1 - ks - w,
+                                       min(valid, p + m.ahead + 1 - ks) - w, m.sinks - ks - w);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          sr[w + c] = see & (1u << c) ? sr[w + c] : __float_as_uint(-INFINITY);
+      }
+    };
+    tmem_ld32(s_addr, s0);
+    tmem_ld32(s_addr + 32, s1);
+    tmem_ld_wait();
+    reg_fence(s0);
+    reg_fence(s1);
+    tmem_ld32(s_addr + 64, s2);
+    tmem_ld32(s_addr + 96, s3);
+    if (edge) hide(0);
+    auto sv = [&](int c) { return __uint_as_float(sr[c]); };
+    float mx8[8];
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx8[a] = fmax3(sv(a), sv(a + 8), sv(a + 16));
+#pragma unroll
+    for (int c = 24; c < 56; c += 16)
+#pragma unroll
+      for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], sv(56 + a));
+    tmem_ld_wait();
+    reg_fence(s2);
+    reg_fence(s3);
+    if (edge) hide(64);
+#pragma unroll
+    for (int c = 64; c < 128; c += 16)
+#pragma unroll
+      for (int a = 0; a < 8; ++a) mx8[a] = fmax3(mx8[a], sv(c + a), sv(c + 8 + a));
+    const float mt = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
+                           fmaxf(mx8[6], mx8[7])) *
+                     scale_log2;
+    // The maximum in use moves only when some row's grew by more than 2^8
+    // (then P stays below 2^8 and O is not rescaled for nothing).  A row
+    // that has seen no key keeps -inf: its factor is 0 and its P below
+    // takes 0.
+    if (__any_sync(0xffffffffu, mt > m_used + 8.f)) {
+      const float m_new = fmaxf(m_used, mt);
+      const float factor = m_used == -INFINITY ? 0.f : exp2_mufu(m_used - m_new);
+      l *= factor;
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)))
+          return false;
+        tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < DH; c += 32) {
-      uint32_t o[32];
-      if (any) {
-        tmem_ld32(o_addr + c, o);
-        tmem_ld_wait();
-        reg_fence(o);
-      } else {
+        for (int c = 0; c < DH; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c, o);
+          tmem_ld_wait();
+          reg_fence(o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
-      }
-      if (any && c + 32 == DH) {  // O_i is in registers: the next unit may overwrite it
-        tc_fence_before();
-        mbar_arrive(&o_free[i]);
-      }
-      if (!live) continue;
-      if (out.o != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint4 u;
-          auto two = [&](int k) {
-            return pack_bf16x2(__uint_as_float(o[e + k]) * inv, __uint_as_float(o[e + k + 1]) * inv);
-          };
-          u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
-          *reinterpret_cast<uint4*>(dst + c + e) = u;
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+          tmem_st32(o_addr + c, o);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4*>(part + c + e) =
-              make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                          __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
       }
+      m_used = m_new;
+    }
+    const float m_sub = m_used == -INFINITY ? 0.f : m_used;
+    const uint64_t cc = f32x2_pack(scale_log2, scale_log2);
+    const uint64_t nm = f32x2_pack(-m_sub, -m_sub);
+    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t xs = f32x2_fma(
+            (static_cast<uint64_t>(sr[32 * q + 2 * e + 1]) << 32) | sr[32 * q + 2 * e], cc, nm);
+        const uint64_t pp = f32x2_pack(exp2_mufu(f32x2_lo(xs)), exp2_mufu(f32x2_hi(xs)));
+        acc2[e & 3] = f32x2_add(acc2[e & 3], pp);
+        pk[e] = pack_bf16x2(f32x2_lo(pp), f32x2_hi(pp));
+      }
+      tmem_st16(s_addr + 16 * q, pk);
+      if (q == 1) {  // the product over the first 64 keys starts now
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_half[i]);
+      }
+    }
+    acc2[0] = f32x2_add(f32x2_add(acc2[0], acc2[1]), f32x2_add(acc2[2], acc2[3]));
+    l += f32x2_lo(acc2[0]) + f32x2_hi(acc2[0]);
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&p_ready[i]);
+    ++n;
+  }
+  // ------------------------------------------------------------ output
+  const bool any = n > 0;
+  if (any && !__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)))
+    return false;
+  tc_fence_after();
+  const int r = cur.row0 + query, h = cur.h0 + head;
+  const bool live = r < cur.row1 && in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH,
+                                              DH, static_cast<int64_t>(dims.H) * DH);
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: o = 0 (O holds no value if n == 0)
+  __nv_bfloat16* dst = out.o + static_cast<int64_t>(r) * out.ld_o + h * DH;
+  float* part = out.part_o + ((static_cast<int64_t>(cur.split) * dims.Lq + r) * dims.H + h) * DH;
+#pragma unroll 1
+  for (int c = 0; c < DH; c += 32) {
+    uint32_t o[32];
+    if (any) {
+      tmem_ld32(o_addr + c, o);
+      tmem_ld_wait();
+      reg_fence(o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = 0;
     }
     if (!live) continue;
-    const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
-    const int64_t at = static_cast<int64_t>(h) * dims.Lq + r;
-    if (out.o == nullptr)
-      out.part_lse[static_cast<int64_t>(cur.split) * dims.H * dims.Lq + at] = lse;
-    else if (out.lse != nullptr)
-      out.lse[at] = lse;
+    if (out.o != nullptr) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 8) {
+        uint4 u;
+        auto two = [&](int k) {
+          return pack_bf16x2(__uint_as_float(o[e + k]) * inv, __uint_as_float(o[e + k + 1]) * inv);
+        };
+        u.x = two(0), u.y = two(2), u.z = two(4), u.w = two(6);
+        *reinterpret_cast<uint4*>(dst + c + e) = u;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4)
+        *reinterpret_cast<float4*>(part + c + e) =
+            make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+    }
   }
+  if (!live) return true;
+  const float lse = l == 0.f ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
+  const int64_t at = static_cast<int64_t>(h) * dims.Lq + r;
+  if (out.o == nullptr)
+    out.part_lse[static_cast<int64_t>(cur.split) * dims.H * dims.Lq + at] = lse;
+  else if (out.lse != nullptr)
+    out.lse[at] = lse;
   return true;
 }
 
@@ -313,8 +295,7 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
   uint8_t* kvbuf = smem + 2 * Cfg::TILE_BYTES;  // stage s: K then V
   uint64_t* bars = reinterpret_cast<uint64_t*>(kvbuf + Cfg::STAGES * 2 * Cfg::TILE_BYTES);
   uint64_t* q_full = bars;
-  uint64_t* q_free = bars + 1;              // a unit's scores are all formed
-  uint64_t* k_full = bars + 2;              // [STAGES]
+  uint64_t* k_full = bars + 1;              // [STAGES]
   uint64_t* v_full = k_full + Cfg::STAGES;  // [STAGES]
   uint64_t* k_empty = v_full + Cfg::STAGES;
   uint64_t* v_empty = k_empty + Cfg::STAGES;
@@ -322,20 +303,18 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
   uint64_t* p_half = s_full + 2;             // [2] P of keys 0..63 stored
   uint64_t* p_ready = p_half + 2;            // [2] all of P stored
   uint64_t* o_done = p_ready + 2;            // [2]
-  uint64_t* o_free = o_done + 2;             // [2] O of a unit that had one has been read
-  uint64_t* mma_done = o_free + 2;
+  uint64_t* mma_done = o_done + 2;
   uint64_t* v_cut = mma_done + 1;            // V tiles whose last rows are zeroed
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(v_cut + 1);
 
   if (out.zero_rest && out.o != nullptr)
     sink_zero_rest(dims.cu_q, dims.B, dims.Lq, out.o, out.ld_o, dims.H * DH);
-  SinkCursor cur;
-  cur.init(dims, cut);
+  SinkUnit cur;
+  if (!cur.init(dims, cut)) return;  // the whole CTA
   const uint32_t warp = warp_id();
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(q_free, 1);
     for (int s = 0; s < Cfg::STAGES; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&v_full[s], 1);
@@ -347,7 +326,6 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
       mbar_init(&p_half[i], 128);
       mbar_init(&p_ready[i], 128);
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 128);
     }
     mbar_init(mma_done, 1);
     mbar_init(v_cut, 1);
@@ -375,67 +353,60 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
     // the whole warp walks the loop (it zeroes rows together); lane 0 issues
     const bool leader = lane_id() == 0;
     const int box = min(cut.rows, 128);
-    int t = 0, t_v = 0, units = 0, cuts = 0;  // K and V tiles, units with tiles, cut tiles
+    if (leader) {
+      mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
+      for (int r = 0; r < 256; r += box)  // `box` rows of one head at a time
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(qbuf + (r >> 7) * Cfg::TILE_BYTES + sl * 16384 + (r & 127) * 128, &qmap,
+                      q_full, (cur.h0 + r / cut.rows) * DH + 64 * sl,
+                      cur.row0 + (r & (cut.rows - 1)));
+    }
+    int issued_k = 0, issued_v = 0, cuts = 0;
     bool ok = true;
-    while (ok && cur.next(dims, cut)) {
-      if (cur.j0 >= cur.j1) continue;
-      if (units > 0) ok = __all_sync(0xffffffffu, mbar_wait(q_free, (units - 1) & 1, budget_ns));
+    for (int j = cur.j0; j < cur.j1; ++j) {
+      const int t = j - cur.j0, s = t % Cfg::STAGES;
+      const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
+      uint8_t* kb = kvbuf + s * 2 * Cfg::TILE_BYTES;
+      uint8_t* vb = kb + Cfg::TILE_BYTES;
+      const int key0 = cur.k0 + cur.kt.start(j);
+      const int valid = cur.kt.valid(j);
+      if (t >= Cfg::STAGES)
+        ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], par, budget_ns));
       if (!ok) break;
       if (leader) {
-        mbar_arrive_expect_tx(q_full, 2 * Cfg::TILE_BYTES);
-        for (int r = 0; r < 256; r += box)  // `box` rows of one head at a time
-          for (int sl = 0; sl < Cfg::SLABS; ++sl)
-            tma_load_2d(qbuf + (r >> 7) * Cfg::TILE_BYTES + sl * 16384 + (r & 127) * 128, &qmap,
-                        q_full, (cur.h0 + r / cut.rows) * DH + 64 * sl,
-                        cur.row0 + (r & (cut.rows - 1)));
+        mbar_arrive_expect_tx(&k_full[s], Cfg::TILE_BYTES);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(kb + sl * 16384, &kmap, &k_full[s], cur.hk * DH + 64 * sl, key0);
+      }
+      ++issued_k;
+      if (t >= Cfg::STAGES)
+        ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], par, budget_ns));
+      if (!ok) break;
+      uint64_t* full = valid < 128 ? v_cut : &v_full[s];
+      if (leader) {
+        mbar_arrive_expect_tx(full, Cfg::TILE_BYTES);
+        for (int sl = 0; sl < Cfg::SLABS; ++sl)
+          tma_load_2d(vb + sl * 16384, &vmap, full, cur.hk * DH + 64 * sl, key0);
       }
       __syncwarp();
-      ++units;
-      for (int j = cur.j0; j < cur.j1; ++j) {
-        const int s = t % Cfg::STAGES;
-        const uint32_t par = ((t / Cfg::STAGES) & 1) ^ 1;
-        uint8_t* kb = kvbuf + s * 2 * Cfg::TILE_BYTES;
-        uint8_t* vb = kb + Cfg::TILE_BYTES;
-        const int key0 = cur.k0 + cur.kt.start(j);
-        const int valid = cur.kt.valid(j);
-        if (t >= Cfg::STAGES)
-          ok = __all_sync(0xffffffffu, mbar_wait(&k_empty[s], par, budget_ns));
+      if (valid < 128) {
+        // the tile lands on a barrier of its own, loses its last rows, and
+        // is then handed on
+        ok = __all_sync(0xffffffffu, mbar_wait(v_cut, cuts & 1, budget_ns));
         if (!ok) break;
-        if (leader) {
-          mbar_arrive_expect_tx(&k_full[s], Cfg::TILE_BYTES);
-          for (int sl = 0; sl < Cfg::SLABS; ++sl)
-            tma_load_2d(kb + sl * 16384, &kmap, &k_full[s], cur.hk * DH + 64 * sl, key0);
-        }
-        ++t;
-        if (t > Cfg::STAGES)
-          ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[s], par, budget_ns));
-        if (!ok) break;
-        uint64_t* full = valid < 128 ? v_cut : &v_full[s];
-        if (leader) {
-          mbar_arrive_expect_tx(full, Cfg::TILE_BYTES);
-          for (int sl = 0; sl < Cfg::SLABS; ++sl)
-            tma_load_2d(vb + sl * 16384, &vmap, full, cur.hk * DH + 64 * sl, key0);
-        }
-        __syncwarp();
-        if (valid < 128) {
-          // the tile lands on a barrier of its own, loses its last rows, and
-          // is then handed on
-          ok = __all_sync(0xffffffffu, mbar_wait(v_cut, cuts & 1, budget_ns));
-          if (!ok) break;
-          ++cuts;
-          sink_zero_rows(vb, Cfg::SLABS, valid);
-          if (leader) mbar_arrive(&v_full[s]);
-        }
-        ++t_v;
+        ++cuts;
+        sink_zero_rows(vb, Cfg::SLABS, valid);
+        if (leader) mbar_arrive(&v_full[s]);
       }
+      ++issued_v;
     }
     if (!ok) record_status(status, kStatusTimeout);
     // no load may be in flight when the CTA ends
-    if (units > 0) mbar_wait(q_full, (units - 1) & 1, 200000000ull);
-    for (int u = max(0, t - Cfg::STAGES); u < t; ++u)
-      mbar_wait(&k_full[u % Cfg::STAGES], (u / Cfg::STAGES) & 1, 200000000ull);
-    for (int u = max(0, t_v - Cfg::STAGES); u < t_v; ++u)
-      mbar_wait(&v_full[u % Cfg::STAGES], (u / Cfg::STAGES) & 1, 200000000ull);
+    mbar_wait(q_full, 0, 200000000ull);
+    for (int t = max(0, issued_k - Cfg::STAGES); t < issued_k; ++t)
+      mbar_wait(&k_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
+    for (int t = max(0, issued_v - Cfg::STAGES); t < issued_v; ++t)
+      mbar_wait(&v_full[t % Cfg::STAGES], (t / Cfg::STAGES) & 1, 200000000ull);
     if (!ok) mbar_wait(v_cut, cuts & 1, 200000000ull);  // a cut tile's load may be in flight
   } else if (warp == 1) {
     // ================================================================ MMA
@@ -443,76 +414,59 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
       constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, DH, false, true);
       const uint32_t qb = smem_u32(qbuf);
-      bool ok = true;
-      int t0 = 0, loads = 0;  // tiles of the units before, units with tiles
-      int done[2] = {0, 0};   // key tiles each row tile has taken, of all units
-      int used[2] = {0, 0};   // units in which it took any
-      while (ok && cur.next(dims, cut)) {
-        auto stage = [&](int j) { return (t0 + j - cur.j0) % Cfg::STAGES; };
-        auto phase = [&](int j) { return ((t0 + j - cur.j0) / Cfg::STAGES) & 1; };
-        auto issue_s = [&](int i, int j) {
-          if (!cur.takes(dims, cut, i, j)) return;
-          const uint32_t kb = smem_u32(kvbuf + stage(j) * 2 * Cfg::TILE_BYTES);
+      bool ok = mbar_wait(q_full, 0, budget_ns);
+      int done[2] = {0, 0};  // key tiles each row tile has taken
+      auto stage = [&](int j) { return (j - cur.j0) % Cfg::STAGES; };
+      auto phase = [&](int j) { return ((j - cur.j0) / Cfg::STAGES) & 1; };
+      auto issue_s = [&](int i, int j) {
+        if (!cur.takes(dims, cut, i, j)) return;
+        const uint32_t kb = smem_u32(kvbuf + stage(j) * 2 * Cfg::TILE_BYTES);
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_ss(tmem + 128 * i, sdesc_sw128(qb + i * Cfg::TILE_BYTES + off, 16, 1024),
-                    sdesc_sw128(kb + off, 16, 1024), idesc_s, kk > 0);
-          }
-          umma_commit(&s_full[i]);
-        };
-        bool begun[2] = {false, false};
-        // O_i += P_i V of tile j, the first 64 keys as soon as their P is there
-        auto issue_o = [&](int i, int j) {
-          if (!cur.takes(dims, cut, i, j)) return true;
-          if (!begun[i]) {  // the O_i of the last unit that had one has been read
-            if (used[i] > 0 && !mbar_wait(&o_free[i], (used[i] - 1) & 1, budget_ns)) return false;
-            ++used[i];
-          }
-          const uint32_t vb =
-              smem_u32(kvbuf + stage(j) * 2 * Cfg::TILE_BYTES + Cfg::TILE_BYTES);
-          for (int half = 0; half < 2; ++half) {
-            if (!mbar_wait(half ? &p_ready[i] : &p_half[i], done[i] & 1, budget_ns)) return false;
-            tc_fence_after();
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_ss(tmem + 128 * i, sdesc_sw128(qb + i * Cfg::TILE_BYTES + off, 16, 1024),
+                  sdesc_sw128(kb + off, 16, 1024), idesc_s, kk > 0);
+        }
+        umma_commit(&s_full[i]);
+      };
+      // O_i += P_i V of tile j, the first 64 keys as soon as their P is there
+      auto issue_o = [&](int i, int j) {
+        if (!cur.takes(dims, cut, i, j)) return true;
+        const uint32_t vb = smem_u32(kvbuf + stage(j) * 2 * Cfg::TILE_BYTES + Cfg::TILE_BYTES);
+        for (int half = 0; half < 2; ++half) {
+          if (!mbar_wait(half ? &p_ready[i] : &p_half[i], done[i] & 1, budget_ns)) return false;
+          tc_fence_after();
 #pragma unroll
-            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-              umma_ts(tmem + 256 + 128 * i, tmem + 128 * i + kk * 8,
-                      sdesc_sw128(vb + kk * 2048, 16384, 1024), idesc_o, begun[i] || kk > 0);
-          }
-          umma_commit(&o_done[i]);
-          begun[i] = true;
-          ++done[i];
-          return true;
-        };
-        if (cur.j0 < cur.j1) {
-          ok = mbar_wait(q_full, loads++ & 1, budget_ns) &&
-               mbar_wait(&k_full[stage(cur.j0)], phase(cur.j0), budget_ns);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(0, cur.j0);
-          issue_s(1, cur.j0);
-          umma_commit(&k_empty[stage(cur.j0)]);
-          if (cur.j0 + 1 == cur.j1) umma_commit(q_free);
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            umma_ts(tmem + 256 + 128 * i, tmem + 128 * i + kk * 8,
+                    sdesc_sw128(vb + kk * 2048, 16384, 1024), idesc_o, done[i] > 0 || kk > 0);
         }
-        for (int j = cur.j0; j < cur.j1; ++j) {
-          const bool more = j + 1 < cur.j1;
-          if (!(ok = mbar_wait(&v_full[stage(j)], phase(j), budget_ns))) break;
+        umma_commit(&o_done[i]);
+        ++done[i];
+        return true;
+      };
+      if (ok && cur.j0 < cur.j1 && (ok = mbar_wait(&k_full[0], 0, budget_ns))) {
+        tc_fence_after();
+        issue_s(0, cur.j0);
+        issue_s(1, cur.j0);
+        umma_commit(&k_empty[0]);
+      }
+      for (int j = cur.j0; j < cur.j1 && ok; ++j) {
+        const bool more = j + 1 < cur.j1;
+        if (!(ok = mbar_wait(&v_full[stage(j)], phase(j), budget_ns))) break;
+        tc_fence_after();
+        if (!(ok = issue_o(0, j))) break;
+        if (more) {
+          if (!(ok = mbar_wait(&k_full[stage(j + 1)], phase(j + 1), budget_ns))) break;
           tc_fence_after();
-          if (!(ok = issue_o(0, j))) break;
-          if (more) {
-            if (!(ok = mbar_wait(&k_full[stage(j + 1)], phase(j + 1), budget_ns))) break;
-            tc_fence_after();
-            issue_s(0, j + 1);
-          }
-          if (!(ok = issue_o(1, j))) break;
-          umma_commit(&v_empty[stage(j)]);
-          if (more) {
-            issue_s(1, j + 1);
-            umma_commit(&k_empty[stage(j + 1)]);
-            if (j + 2 == cur.j1) umma_commit(q_free);
-          }
+          issue_s(0, j + 1);
         }
-        t0 += cur.j1 - cur.j0;
+        if (!(ok = issue_o(1, j))) break;
+        umma_commit(&v_empty[stage(j)]);
+        if (more) {
+          issue_s(1, j + 1);
+          umma_commit(&k_empty[stage(j + 1)]);
+        }
       }
       if (!ok) record_status(status, kStatusTimeout);
       umma_commit(mma_done);
@@ -521,7 +475,7 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
     // ================================================================ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n" ::: "memory");
     if (!sink_softmax<DH>((warp - 4) >> 2, tmem, cur, dims, cut, s_full, o_done, p_half, p_ready,
-                          o_free, scale_log2, out, status, budget_ns))
+                          scale_log2, out, status, budget_ns))
       record_status(status, kStatusTimeout);
   }
 
@@ -621,12 +575,9 @@ cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, const SinkCut& 
   out.part_lse = reinterpret_cast<float*>(
       ws + kStatusBytes +
       align256(static_cast<size_t>(splits) * dims.Lq * dims.H * DH * sizeof(float)));
-  const int64_t units = static_cast<int64_t>(sink_slots(dims.Lq, dims.B, cut.rows)) *
-                        (dims.H * cut.rows / 256) * splits;
-  const int sms = sm_count_of_current_device();
-  sink_attn_kernel<DH><<<static_cast<unsigned>(units < sms ? units : sms), Cfg::THREADS, Cfg::SMEM,
-                         ctx.stream>>>(qmap, kmap, vmap, dims, cut, scale * 1.4426950408889634f,
-                                       out, ctx.status, ctx.budget_ns);
+  const int grid = sink_slots(dims.Lq, dims.B, cut.rows) * (dims.H * cut.rows / 256) * splits;
+  sink_attn_kernel<DH><<<grid, Cfg::THREADS, Cfg::SMEM, ctx.stream>>>(
+      qmap, kmap, vmap, dims, cut, scale * 1.4426950408889634f, out, ctx.status, ctx.budget_ns);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (splits > 1) {
     const int64_t warps = static_cast<int64_t>(dims.Lq) * dims.H;
@@ -703,7 +654,9 @@ vdn_status vdn_sink_attn(const vdn_sink_shape* shape, const void* q, int64_t ld_
     return VDN_ERR_WORKSPACE;
   if (s.Lq == 0) return VDN_OK;
   const SinkCut cut = sink_cut(s);
-  if (static_cast<int64_t>(s.Lq) * s.H >= (int64_t(1) << 33))
+  if (static_cast<int64_t>(sink_slots(s.Lq, s.B, cut.rows)) * s.H * cut.splits >=
+          (int64_t(1) << 31) ||
+      static_cast<int64_t>(s.Lq) * s.H >= (int64_t(1) << 33))
     return VDN_ERR_UNSUPPORTED;
   const SinkDims dims{s.Lq, s.Lk, s.B, s.H, s.H_kv, cu_q, cu_k, {s.window, s.ahead, s.sinks}};
   CUtensorMap qmap, kmap, vmap;

@@ -715,38 +715,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // dK and dV of the units that several CTAs share: the sum of their parts, the
-// CTA with the unit's first items first.
+// CTA with the unit's first items first.  blockIdx.x: the CTA whose begin is
+// the first inside the unit, if there is one.
 template <int DH>
 __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, const KeyPass a,
                                                         float scale) {
   const SinkPlan* p = a.plan;
-  const int slot = blockIdx.x / dims.Hkv, hk = blockIdx.x % dims.Hkv;
+  const int c1 = blockIdx.x + 1;
+  if (c1 >= p->ctas) return;
+  const int slot = p->start[c1];
+  const int64_t x1 = p->first[c1], x0 = p->first[c1 - 1], at = p->before[slot] * dims.Hkv;
   const SlotRec r = p->rec[slot];
   if (r.tile < 0) return;
   const int64_t weight = r.tiles * (dims.H / dims.Hkv) + kUnitCost;
-  const int64_t begin = p->before[slot] * dims.Hkv + hk * weight, last = begin + weight - 1;
-  auto owner = [&](int64_t x) {  // the last CTA that begins at or before x
-    int lo = 0, hi = p->ctas;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p->first[mid] <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    return lo;
-  };
-  const int first = owner(begin), end = owner(last);
-  if (first == end) return;
+  const int hk = static_cast<int>((x1 - at) / weight);
+  const int64_t begin = at + hk * weight;
+  if (hk >= dims.Hkv || x1 == begin || x0 > begin) return;
   const SinkSeq seq = sink_seq(dims, r.b);
   // blockIdx.y: dV or dK, and 16 of the 128 keys; a thread: 8 columns of a key
   const int which = blockIdx.y >> 3;
   const int row = (blockIdx.y & 7) * 16 + threadIdx.x / (DH / 8), c0 = threadIdx.x % (DH / 8) * 8;
   if (threadIdx.x >= 16 * (DH / 8) || 128 * r.tile + row >= seq.nk()) return;
   float x[8] = {};
-  for (int c = first; c <= end; ++c) {
+  for (int c = c1 - 1; c < p->ctas && p->first[c] < begin + weight; ++c) {
     const float4* in = reinterpret_cast<const float4*>(
-        a.part + ((static_cast<int64_t>(c) * 2 + (c == first)) * 2 + which) * (DH * 128) +
+        a.part + ((static_cast<int64_t>(c) * 2 + (c < c1)) * 2 + which) * (DH * 128) +
         row * DH + c0);
     const float4 u = in[0], v = in[1];
     x[0] += u.x, x[1] += u.y, x[2] += u.z, x[3] += u.w;
@@ -1102,9 +1095,10 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
     sink_key_pass_kernel<DH><<<ctas, kThreads, Cfg::SMEM, ctx.stream>>>(
         t.q, t.d_o, t.k, t.v, dims, a, scale, ctx.status, ctx.budget_ns);
     if (cudaError_t e = cudaGetLastError()) return e;
-    sink_join_kernel<DH><<<dim3(sink_slots(dims.Lk, dims.B, 128) * dims.Hkv, 16), 256, 0,
-                           ctx.stream>>>(dims, a, scale);
-    if (cudaError_t e = cudaGetLastError()) return e;
+    if (ctas > 1) {
+      sink_join_kernel<DH><<<dim3(ctas - 1, 16), 256, 0, ctx.stream>>>(dims, a, scale);
+      if (cudaError_t e = cudaGetLastError()) return e;
+    }
   }
   if (dims.Lq > 0)
     sink_query_pass_kernel<DH><<<q_slots * dims.H, kThreads, Cfg::SMEM, ctx.stream>>>(
