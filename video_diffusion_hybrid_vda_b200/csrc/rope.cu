@@ -18,19 +18,31 @@
 // cos/sin of its few rows once into shared memory and all heads of those rows
 // use them (64 sines a row against 48 x 128 elements at 24 + 24 heads).  One
 // thread holds both members of its pairs (two vectors of V elements), so the
-// rotation needs no exchange; the head's sum is a shuffle over its lanes.
+// rotation needs no exchange; the head's sum is a shuffle over its lanes.  A
+// thread keeps its row and its columns and walks the heads, so the turns and
+// the norm's weights stay in registers (read again for every head from shared
+// memory and L1: 42336 rows of 24 + 24 heads of 128 took 234 us).  What keeps
+// the memory busy is bytes in flight: loads go through a cp.async ring in
+// shared memory in which every thread has its own slots (no barrier), so they
+// cost no registers (prefetched into registers: 208 us; now 179 us, 5.8 TB/s).
+// Blocks that walk row groups in turn instead of one group a block: 207 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace vdn {
 
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kStages = 3;           // forward: heads in the ring (x: two vectors)
+constexpr int kBwdStages = 2;        // backward (x and dy: four)
+// its ring of 16-byte vectors and the turns of 16 rows of 128 pairs
+constexpr int kBwdSmemMax = kBwdStages * 4 * kThreads * 16 + 16 * 128 * 8;
 constexpr int kMaxBwdBlocks = 1024;  // rows of the weight-gradient partials
 
 struct Side {            // queries or keys
@@ -77,6 +89,24 @@ __device__ __forceinline__ void store_words(void* p, const uint32_t (&u)[WORDS])
     *static_cast<uint2*>(p) = make_uint2(u[0], u[1]);
 }
 
+// Asynchronous copy of one vector into this thread's slot of the ring.
+template <int WORDS>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (WORDS == 4)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <typename T, int V, int WORDS>
 __device__ __forceinline__ void unpack(const uint32_t (&u)[WORDS], float (&f)[V]) {
   if constexpr (sizeof(T) == 4) {
@@ -114,12 +144,9 @@ __device__ __forceinline__ void pack(const float (&f)[V], uint32_t (&u)[WORDS]) 
   }
 }
 
-// cos/sin of rows [r0, r0 + n) into shared memory.  Unit u's V pairs lie as
-// V/2 float4s (cos, sin, cos, sin) at [j][u], so that neighbouring lanes read
-// neighbouring 16 bytes.
-template <int V>
+// cos/sin of rows [r0, r0 + n) into shared memory, [row][pair].
 __device__ __forceinline__ void fill_turns(const RopeArgs& a, float2* cs, int64_t r0, int n) {
-  const int pairs = a.rot / 2, units = pairs / V;
+  const int pairs = a.rot / 2;
   for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
     const int row = i / pairs, pair = i - row * pairs;
     const int axis = (pair >= a.sec1) + (pair >= a.sec2) + (pair >= a.sec3);
@@ -129,33 +156,44 @@ __device__ __forceinline__ void fill_turns(const RopeArgs& a, float2* cs, int64_
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &sn,
               &cn);  // 2^-31: half turns
-    const int u = pair / V, e = pair - u * V;
-    cs[row * pairs + ((e >> 1) * units + u) * 2 + (e & 1)] =
-        make_float2(cn * a.scale, sn * a.scale * a.sin_sign);
+    cs[row * pairs + pair] = make_float2(cn * a.scale, sn * a.scale * a.sin_sign);
   }
 }
 
-// Turn the unit's pairs by the row's cos/sin (sign: the sine's factor).
+// The turns of a unit's pairs in one row, (cos, sin, cos, sin) of two pairs a
+// float4: pair e of the half layout joins element e of both vectors; in the
+// interleaved layout the first V / 2 pairs lie in the vector at column ca, the
+// others in that at cb.  Columns past the rotated ones turn by nothing.
 template <int V, bool INTER>
-__device__ __forceinline__ void turn_unit(const float2* cs, int u, int units, float (&fa)[V],
-                                          float (&fb)[V]) {
-  const float4* c4 = reinterpret_cast<const float4*>(cs);
+__device__ __forceinline__ void load_turns(const float2* cs, int rot, int ca, int cb,
+                                           float4 (&c)[V / 2]) {
+  const float4* p = reinterpret_cast<const float4*>(cs);
 #pragma unroll
   for (int j = 0; j < V / 2; ++j) {
-    const float4 c = c4[j * units + u];  // pairs 2j, 2j+1 of the unit
-    auto rot2 = [](float& x, float& y, float cn, float sn) {
-      const float t = x * cn - y * sn;
-      y = y * cn + x * sn;
-      x = t;
-    };
+    const int col = INTER ? (j < V / 4 ? ca + 4 * j : cb + 4 * j - V) : ca;
+    c[j] = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (col < (INTER ? rot : rot / 2)) c[j] = INTER ? p[col / 4] : p[ca / 2 + j];
+  }
+}
+
+template <int V, bool INTER>
+__device__ __forceinline__ void turn_unit(const float4 (&c)[V / 2], float (&fa)[V],
+                                          float (&fb)[V]) {
+  auto turn = [](float& x, float& y, float cn, float sn) {
+    const float t = x * cn - y * sn;
+    y = y * cn + x * sn;
+    x = t;
+  };
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) {
     if constexpr (INTER) {
-      float(&f)[V] = 4 * j < V ? fa : fb;
+      float(&f)[V] = j < V / 4 ? fa : fb;
       const int e = (4 * j) % V;
-      rot2(f[e], f[e + 1], c.x, c.y);
-      rot2(f[e + 2], f[e + 3], c.z, c.w);
+      turn(f[e], f[e + 1], c[j].x, c[j].y);
+      turn(f[e + 2], f[e + 3], c[j].z, c[j].w);
     } else {
-      rot2(fa[2 * j], fb[2 * j], c.x, c.y);
-      rot2(fa[2 * j + 1], fb[2 * j + 1], c.z, c.w);
+      turn(fa[2 * j], fb[2 * j], c[j].x, c[j].y);
+      turn(fa[2 * j + 1], fb[2 * j + 1], c[j].z, c[j].w);
     }
   }
 }
@@ -179,101 +217,111 @@ __device__ __forceinline__ void load_weight(const float* w, int col, float (&f)[
   }
 }
 
-// Columns of unit u's two vectors.
+// Columns of unit u's two vectors: side by side with the neighbouring lanes'
+// in both, and in the half layout the two members of its pairs.
 template <int V, bool INTER>
 __device__ __forceinline__ void unit_columns(int u, int d, int rot, int& ca, int& cb) {
-  if (!INTER && 2 * V * u < rot) {
-    ca = u * V;
-    cb = rot / 2 + u * V;
-  } else {
-    ca = 2 * V * u;
-    cb = ca + V;
+  ca = u * V;
+  if (INTER) {
+    cb = d / 2 + u * V;
+  } else if (2 * ca < rot) {
+    cb = rot / 2 + ca;
+  } else {  // the columns that pass through, in two runs of their own
+    ca += rot / 2;
+    cb = ca + (d - rot) / 2;
   }
 }
 
-template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, int V, bool INTER, bool NORM>
+__global__ void __launch_bounds__(kThreads, NORM ? 3 : 4)
+    rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ float4 smem_f4[];
-  float2* cs = reinterpret_cast<float2*>(smem_f4);
   constexpr int W = V * static_cast<int>(sizeof(T)) / 4;
+  constexpr int SLOT = kThreads * W * 4;  // bytes of one vector of all threads
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem_f4);
+  float2* cs = reinterpret_cast<float2*>(ring + kStages * 2 * SLOT);
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * a.rows_per_block;
   const int n = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - r0));
-  const int heads = a.s[0].heads + a.s[1].heads;
-  const int total = n * heads;
-  const int step = kThreads / a.lanes;
-  const int u = threadIdx.x & (a.lanes - 1);
-  const bool live = u < a.d / (2 * V);
-  const bool turned = 2 * V * u < a.rot;
+  // thread: unit u of a head; its row, and every `step`-th head from `first`
+  const int u = threadIdx.x & (a.lanes - 1), slot = threadIdx.x / a.lanes;
+  const int step = kThreads / a.lanes / a.rows_per_block;
+  const int row = slot / step, first = slot & (step - 1);  // neighbouring heads side by side
+  const bool live = row < n && u < a.d / (2 * V);
   int ca, cb;
   unit_columns<V, INTER>(u, a.d, a.rot, ca, cb);
-
-  auto address = [&](int slot, int& row, bool& key) {
-    row = slot / heads;
-    const int h = slot - row * heads;
-    key = h >= a.s[0].heads;
-    return static_cast<int64_t>(key ? h - a.s[0].heads : h) * a.d;
-  };
-  uint32_t na[W], nb[W];
-  auto fetch = [&](int slot) {
-    if (slot >= total || !live) return;
-    int row;
-    bool key;
-    const int64_t off = address(slot, row, key);
-    const Side& s = key ? a.s[1] : a.s[0];
-    const T* src = static_cast<const T*>(s.x) + (r0 + row) * s.ldx + off;
-    load_words<W>(src + ca, na);
-    load_words<W>(src + cb, nb);
+  const bool turned = ca < (INTER ? a.rot : a.rot / 2);
+  // passes over the heads of the queries, then of the keys
+  const int passes_q = (a.s[0].heads + step - 1) / step;
+  const int passes = passes_q + (a.s[1].heads + step - 1) / step;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * W * 4;
+  auto fetch = [&](int k) {
+    const bool key = k >= passes_q;
+    const Side& s = a.s[key];
+    const int h = (key ? k - passes_q : k) * step + first;
+    if (k < passes && live && h < s.heads) {
+      const T* src = static_cast<const T*>(s.x) + (r0 + row) * s.ldx +
+                     static_cast<int64_t>(h) * a.d;
+      const uint32_t dst = mine + k % kStages * 2 * SLOT;
+      copy_async<W>(dst, src + ca);
+      copy_async<W>(dst + SLOT, src + cb);
+    }
+    copy_commit();
   };
   // the first loads are in flight while the block computes its angles
-  const int first = threadIdx.x / a.lanes;
-  fetch(first);
-  if (a.rot > 0) fill_turns<V>(a, cs, r0, n);
-  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kStages - 1; ++k) fetch(k);
+  float4 turns[V / 2];
+  if (a.rot > 0) {
+    fill_turns(a, cs, r0, n);
+    __syncthreads();
+    if (live && turned) load_turns<V, INTER>(cs + row * (a.rot / 2), a.rot, ca, cb, turns);
+  }
+  float wa[V], wb[V];
   // the trip count is the block's, since the sums are warp-collective
-  for (int base = 0; base < total; base += step) {
-    const int slot = base + first;
-    const bool on = live && slot < total;
+  for (int k = 0; k < passes; ++k) {
+    const bool key = k >= passes_q;
+    const Side& s = a.s[key];
+    const int h = (key ? k - passes_q : k) * step + first;
+    const bool on = live && h < s.heads;
+    if (NORM && live && (k == 0 || k == passes_q)) {
+      load_weight<V>(s.w, ca, wa);
+      load_weight<V>(s.w, cb, wb);
+    }
+    fetch(k + kStages - 1);
+    copy_wait<kStages - 1>();
     float fa[V], fb[V];
     if (on) {
-      unpack<T, V, W>(na, fa);
-      unpack<T, V, W>(nb, fb);
+      uint32_t xa[W], xb[W];
+      const uint8_t* src = ring + k % kStages * 2 * SLOT + threadIdx.x * W * 4;
+      load_words<W>(src, xa);
+      load_words<W>(src + SLOT, xb);
+      unpack<T, V, W>(xa, fa);
+      unpack<T, V, W>(xb, fb);
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e) fa[e] = fb[e] = 0.f;
     }
-    fetch(slot + step);
-    int row;
-    bool key;
-    const int64_t off = address(on ? slot : 0, row, key);
-    const Side& s = key ? a.s[1] : a.s[0];
-    if (a.s[0].norm | a.s[1].norm) {
+    if (NORM && s.norm != VDN_NORM_NONE) {
       float q = 0.f;
 #pragma unroll
       for (int e = 0; e < V; ++e) q += fa[e] * fa[e] + fb[e] * fb[e];
       q = lane_sum(q, a.lanes);
-      if (s.norm != VDN_NORM_NONE && on) {
-        const float r =
-            rsqrtf(q * (s.norm == VDN_NORM_RMS ? 1.f / static_cast<float>(a.d) : 1.f) + a.eps);
-        float wa[V], wb[V];
-        load_weight<V>(s.w, ca, wa);
-        load_weight<V>(s.w, cb, wb);
+      const float r =
+          rsqrtf(q * (s.norm == VDN_NORM_RMS ? 1.f / static_cast<float>(a.d) : 1.f) + a.eps);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          fa[e] *= r * wa[e];
-          fb[e] *= r * wb[e];
-        }
+      for (int e = 0; e < V; ++e) {
+        fa[e] *= r * wa[e];
+        fb[e] *= r * wb[e];
       }
     }
-    if (on) {
-      if (turned)
-        turn_unit<V, INTER>(cs + row * (a.rot / 2), u, a.rot / (2 * V), fa, fb);
-      uint32_t oa[W], ob[W];
-      pack<T, V, W>(fa, oa);
-      pack<T, V, W>(fb, ob);
-      T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + off;
-      store_words<W>(dst + ca, oa);
-      store_words<W>(dst + cb, ob);
-    }
+    if (!on) continue;
+    if (turned) turn_unit<V, INTER>(turns, fa, fb);
+    uint32_t oa[W], ob[W];
+    pack<T, V, W>(fa, oa);
+    pack<T, V, W>(fb, ob);
+    T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + static_cast<int64_t>(h) * a.d;
+    store_words<W>(dst + ca, oa);
+    store_words<W>(dst + cb, ob);
   }
 }
 
@@ -285,65 +333,91 @@ template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
     const __grid_constant__ RopeArgs a) {
   extern __shared__ float4 smem_f4[];
-  float2* cs = reinterpret_cast<float2*>(smem_f4);
   constexpr int W = V * static_cast<int>(sizeof(T)) / 4;
+  constexpr int SLOT = kThreads * W * 4;  // bytes of one vector of all threads
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem_f4);
+  float2* cs = reinterpret_cast<float2*>(ring + kBwdStages * 4 * SLOT);
   const bool key = static_cast<int>(blockIdx.x) >= a.blocks_q;
   const Side& s = a.s[key ? 1 : 0];
   const int blk = key ? blockIdx.x - a.blocks_q : blockIdx.x;
   const int nblk = key ? gridDim.x - a.blocks_q : a.blocks_q;
-  const int step = kThreads / a.lanes;
-  const int u = threadIdx.x & (a.lanes - 1);
-  const bool live = u < a.d / (2 * V);
-  const bool turned = 2 * V * u < a.rot;
+  const int u = threadIdx.x & (a.lanes - 1), slot = threadIdx.x / a.lanes;
+  const int step = kThreads / a.lanes / a.rows_per_block;
+  const int row = slot / step, first = slot & (step - 1);  // neighbouring heads side by side
+  const bool unit = u < a.d / (2 * V);
   const float c = s.norm == VDN_NORM_RMS ? 1.f / static_cast<float>(a.d) : 1.f;
   int ca, cb;
   unit_columns<V, INTER>(u, a.d, a.rot, ca, cb);
+  const bool turned = ca < (INTER ? a.rot : a.rot / 2);
   float wa[V], wb[V], da[V], db[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) wa[e] = wb[e] = 1.f, da[e] = db[e] = 0.f;
-  if (live) {
+  if (unit) {
     load_weight<V>(s.w, ca, wa);
     load_weight<V>(s.w, cb, wb);
   }
-  const int first = threadIdx.x / a.lanes;
-  for (int64_t r0 = static_cast<int64_t>(blk) * a.rows_per_block; r0 < a.rows;
-       r0 += static_cast<int64_t>(nblk) * a.rows_per_block) {
+  // one run of passes over the heads of the block's row groups, so that the
+  // ring does not drain between groups
+  const int64_t groups = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
+  const int64_t my_groups = blk < groups ? (groups - blk + nblk - 1) / nblk : 0;
+  const int passes = (s.heads + step - 1) / step;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * W * 4;
+  int64_t fg = 0;  // the next fetch: group (of this block's), pass and stage
+  int fk = 0, fs = 0;
+  auto fetch = [&] {
+    const int64_t r = (blk + fg * nblk) * a.rows_per_block + row;
+    const int h = fk * step + first;
+    if (fg < my_groups && unit && r < a.rows && h < s.heads) {
+      const int64_t off = static_cast<int64_t>(h) * a.d;
+      const T* x = static_cast<const T*>(s.x) + r * s.ldx + off;
+      const T* g = static_cast<const T*>(s.g) + r * s.ldg + off;
+      const uint32_t dst = mine + fs * 4 * SLOT;
+      copy_async<W>(dst, x + ca);
+      copy_async<W>(dst + SLOT, x + cb);
+      copy_async<W>(dst + 2 * SLOT, g + ca);
+      copy_async<W>(dst + 3 * SLOT, g + cb);
+    }
+    copy_commit();
+    if (++fk == passes) fk = 0, ++fg;
+    if (++fs == kBwdStages) fs = 0;
+  };
+#pragma unroll
+  for (int k = 0; k < kBwdStages - 1; ++k) fetch();
+  int stage = 0;
+  for (int64_t group = 0; group < my_groups; ++group) {
+    const int64_t r0 = (blk + group * nblk) * a.rows_per_block;
     const int n = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - r0));
-    const int total = n * s.heads;
-    uint32_t xa[W], xb[W], ga[W], gb[W];
-    auto fetch = [&](int slot) {
-      if (slot >= total || !live) return;
-      const int row = slot / s.heads;
-      const int64_t off = static_cast<int64_t>(slot - row * s.heads) * a.d;
-      const T* x = static_cast<const T*>(s.x) + (r0 + row) * s.ldx + off;
-      const T* g = static_cast<const T*>(s.g) + (r0 + row) * s.ldg + off;
-      load_words<W>(x + ca, xa);
-      load_words<W>(x + cb, xb);
-      load_words<W>(g + ca, ga);
-      load_words<W>(g + cb, gb);
-    };
-    fetch(first);
-    __syncthreads();  // the previous group's turns have been read
-    if (a.rot > 0) fill_turns<V>(a, cs, r0, n);
-    __syncthreads();
-    for (int base = 0; base < total; base += step) {
-      const int slot = base + first;
-      const bool on = live && slot < total;
+    const bool live = unit && row < n;
+    float4 turns[V / 2];
+    if (a.rot > 0) {
+      __syncthreads();  // the previous group's turns have been read
+      fill_turns(a, cs, r0, n);
+      __syncthreads();
+      if (live && turned) load_turns<V, INTER>(cs + row * (a.rot / 2), a.rot, ca, cb, turns);
+    }
+    for (int k = 0; k < passes; ++k) {
+      const int h = k * step + first;
+      const bool on = live && h < s.heads;
+      fetch();
+      copy_wait<kBwdStages - 1>();
       float fxa[V], fxb[V], fga[V], fgb[V];
       if (on) {
-        unpack<T, V, W>(xa, fxa);
-        unpack<T, V, W>(xb, fxb);
-        unpack<T, V, W>(ga, fga);
-        unpack<T, V, W>(gb, fgb);
+        uint32_t v[W];
+        const uint8_t* src = ring + stage * 4 * SLOT + threadIdx.x * W * 4;
+        load_words<W>(src, v);
+        unpack<T, V, W>(v, fxa);
+        load_words<W>(src + SLOT, v);
+        unpack<T, V, W>(v, fxb);
+        load_words<W>(src + 2 * SLOT, v);
+        unpack<T, V, W>(v, fga);
+        load_words<W>(src + 3 * SLOT, v);
+        unpack<T, V, W>(v, fgb);
+        if (turned) turn_unit<V, INTER>(turns, fga, fgb);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) fxa[e] = fxb[e] = fga[e] = fgb[e] = 0.f;
       }
-      fetch(slot + step);
-      const int row = on ? slot / s.heads : 0;
-      const int64_t off = static_cast<int64_t>(slot - row * s.heads) * a.d;
-      if (on && turned)
-        turn_unit<V, INTER>(cs + row * (a.rot / 2), u, a.rot / (2 * V), fga, fgb);
+      if (++stage == kBwdStages) stage = 0;
       float r = 1.f, back = 0.f;
       if (s.norm != VDN_NORM_NONE) {
         float q = 0.f, t = 0.f;
@@ -370,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
         uint32_t pa[W], pb[W];
         pack<T, V, W>(oa, pa);
         pack<T, V, W>(ob, pb);
-        T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + off;
+        T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + static_cast<int64_t>(h) * a.d;
         store_words<W>(dst + ca, pa);
         store_words<W>(dst + cb, pb);
       }
@@ -378,38 +452,41 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
   }
   if (a.partial == nullptr) return;
   __syncthreads();
-  float* sum = reinterpret_cast<float*>(smem_f4);  // [step][d]
-  if (live) {
+  float* sum = reinterpret_cast<float*>(smem_f4);  // [slots][d]
+  const int slots = kThreads / a.lanes;
+  if (unit) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      sum[first * a.d + ca + e] = da[e];
-      sum[first * a.d + cb + e] = db[e];
+      sum[slot * a.d + ca + e] = da[e];
+      sum[slot * a.d + cb + e] = db[e];
     }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < a.d; i += kThreads) {
     float t = 0.f;
-    for (int j = 0; j < step; ++j) t += sum[j * a.d + i];
+    for (int j = 0; j < slots; ++j) t += sum[j * a.d + i];
     a.partial[static_cast<int64_t>(blockIdx.x) * a.d + i] = t;
   }
 }
 
-// dw[i] = sum of the partials' rows, in a fixed order: 8 columns a block (one
-// per warp), a lane takes every 32nd row.
-__global__ void __launch_bounds__(kThreads) rope_dw_kernel(const float* partial, int d,
-                                                           int blocks_q, int blocks, float* dwq,
-                                                           float* dwk) {
+// dw[i] = sum of the partials' rows, in a fixed order: a block takes 32
+// columns, warp w every 32nd row from row w.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int d, int blocks_q,
+                                                       int blocks, float* dwq, float* dwk) {
+  __shared__ float sums[32][33];
   const bool key = blockIdx.y == 1;
   float* dw = key ? dwk : dwq;
-  const int col = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (dw == nullptr || col >= d) return;
-  const int lane = threadIdx.x & 31;
+  if (dw == nullptr) return;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, col = blockIdx.x * 32 + lane;
   const int b1 = key ? blocks : blocks_q;
   float t = 0.f;
-  for (int b = (key ? blocks_q : 0) + lane; b < b1; b += 32)
-    t += partial[static_cast<int64_t>(b) * d + col];
-  t = lane_sum(t, 32);
-  if (lane == 0) dw[col] = t;
+#pragma unroll 4
+  for (int b = (key ? blocks_q : 0) + w; b < b1; b += 32)
+    t += col < d ? partial[static_cast<int64_t>(b) * d + col] : 0.f;
+  sums[w][lane] = t;
+  __syncthreads();
+  t = lane_sum(sums[lane][w], 32);  // column w of the block
+  if (lane == 0 && blockIdx.x * 32 + w < d) dw[blockIdx.x * 32 + w] = t;
 }
 
 bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
@@ -495,25 +572,41 @@ vdn_status check_side(const Side& s, int d, int64_t rows, bool backward) {
   return VDN_OK;
 }
 
-// Rows of a block: enough that every thread computes about one sine and
-// cosine, but no more than leaves four blocks an SM.
-int rows_per_block(int64_t rows, int rot, int sms) {
-  int n = rot > 0 ? 2 * kThreads / rot : 4;
-  n = n < 1 ? 1 : n > 8 ? 8 : n;
-  while (n > 1 && (rows + n - 1) / n < 4 * sms) n /= 2;
-  return n;
+// Rows of a block (a power of two): of its slots (a head's lanes each) so many
+// take different rows and the rest different heads that the fewest are left
+// over in the last pass over the heads; of equal choices the one nearest 8
+// from below, since a block's start-up is paid once for its rows (24 + 24 heads
+// of 128, 42336 rows: 350 us with one row, 268 with 2, 209 with 4, 194 with
+// 8), and fewer rows where the GPU would have less than two blocks an SM.
+int rows_per_block(int64_t rows, int lanes, int heads0, int heads1, int sms) {
+  const int slots = kThreads / lanes;
+  int best = 1, least = 1 << 30;
+  for (int n = 1; n <= slots && n <= 16; n *= 2) {
+    const int step = slots / n;  // heads a pass
+    const int cost = ((heads0 + step - 1) / step + (heads1 + step - 1) / step) * step;
+    if (cost < least || (cost == least && n <= 8)) best = n, least = cost;
+  }
+  while (best > 1 && (rows + best - 1) / best < 2 * sms) best /= 2;
+  return best;
 }
 
 vdn_status launch_forward(RopeArgs& a, int dtype, int layout, cudaStream_t stream) {
   if (a.rows == 0) return VDN_OK;
-  a.rows_per_block = rows_per_block(a.rows, a.rot, sm_count_of_current_device());
-  const int smem = a.rows_per_block * a.rot / 2 * 8;
+  a.rows_per_block = rows_per_block(a.rows, a.lanes, a.s[0].heads, a.s[1].heads,
+                                    sm_count_of_current_device());
+  const int vec = vector_width(dtype, a.d, a.rot) * (dtype == VDN_DTYPE_F32 ? 4 : 2);
+  const int smem = kStages * 2 * kThreads * vec + a.rows_per_block * a.rot / 2 * 8;
   const int64_t grid = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
   const cudaError_t e = dispatch(
       dtype, vector_width(dtype, a.d, a.rot), layout == VDN_ROPE_INTERLEAVED,
       [&](auto t, auto v, auto inter) {
-        rope_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>
-            <<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+        using T = decltype(t);
+        constexpr int V = decltype(v)::value;
+        constexpr bool I = decltype(inter)::value;
+        if (a.s[0].norm | a.s[1].norm)
+          rope_kernel<T, V, I, true><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
+        else
+          rope_kernel<T, V, I, false><<<static_cast<unsigned>(grid), kThreads, smem, stream>>>(a);
         return cudaGetLastError();
       });
   return e == cudaSuccess ? VDN_OK : VDN_ERR_CUDA;
@@ -593,7 +686,7 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
                   ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes)
                   : nullptr;
   const int sms = sm_count_of_current_device();
-  a.rows_per_block = rows_per_block(rows, a.rot, sms);
+  a.rows_per_block = rows_per_block(rows, a.lanes, H, H_kv, sms);
   // blocks shared out by heads; at most four an SM, at most one a row group
   const int64_t groups = (rows + a.rows_per_block - 1) / a.rows_per_block;
   const int most = 4 * sms < kMaxBwdBlocks ? 4 * sms : kMaxBwdBlocks - 1;  // each side has one
@@ -604,18 +697,23 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
   };
   a.blocks_q = share(H);
   const int blocks = a.blocks_q + share(H_kv);
-  const int turns = a.rows_per_block * a.rot / 2 * 8;
+  const int vec = vector_width(dtype, a.d, a.rot) * (dtype == VDN_DTYPE_F32 ? 4 : 2);
+  const int ring = kBwdStages * 4 * kThreads * vec + a.rows_per_block * a.rot / 2 * 8;
   const int sums = kThreads / a.lanes * a.d * 4;
   const cudaError_t e = dispatch(
       dtype, vector_width(dtype, a.d, a.rot), plan->layout == VDN_ROPE_INTERLEAVED,
       [&](auto t, auto v, auto inter) {
-        rope_backward_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>
-            <<<blocks, kThreads, turns > sums ? turns : sums, st>>>(a);
+        const auto kernel =
+            rope_backward_kernel<decltype(t), decltype(v)::value, decltype(inter)::value>;
+        const int smem = ring > sums ? ring : sums;
+        static std::atomic<uint64_t> smem_set{0};  // one for each kernel
+        if (cudaError_t e = set_smem_once(kernel, kBwdSmemMax, smem_set)) return e;
+        kernel<<<blocks, kThreads, smem, st>>>(a);
         return cudaGetLastError();
       });
   if (e != cudaSuccess) return VDN_ERR_CUDA;
   if (a.partial != nullptr) {
-    rope_dw_kernel<<<dim3((a.d + 7) / 8, 2), kThreads, 0, st>>>(a.partial, a.d, a.blocks_q,
+    rope_dw_kernel<<<dim3((a.d + 31) / 32, 2), 1024, 0, st>>>(a.partial, a.d, a.blocks_q,
                                                                 blocks, dwq, dwk);
     if (cudaGetLastError() != cudaSuccess) return VDN_ERR_CUDA;
   }

@@ -29,6 +29,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "exp2_fma.cuh"
 #include "sink_attn.cuh"
 
@@ -516,19 +518,23 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
   float sum = f;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  using Vec = std::conditional_t<W == 4, float4, float2>;
   float acc[W] = {};
-  const float* src = parts.part_o + (static_cast<int64_t>(r) * dims.H + h) * DH + lane;
+  const Vec* src = reinterpret_cast<const Vec*>(
+                       parts.part_o + (static_cast<int64_t>(r) * dims.H + h) * DH) + lane;
 #pragma unroll 8
   for (int s = 0; s < splits; ++s) {
     const float fs = __shfl_sync(0xffffffffu, f, s);
+    const Vec v = src[s * step * 32];
+    const float* x = reinterpret_cast<const float*>(&v);
 #pragma unroll
-    for (int c = 0; c < W; ++c) acc[c] += fs * src[32 * c];
-    src += step * DH;
+    for (int c = 0; c < W; ++c) acc[c] += fs * x[c];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(r) * ld_o + h * DH) +
+                  W / 2 * lane;
 #pragma unroll
-  for (int c = 0; c < W; ++c)
-    o[static_cast<int64_t>(r) * ld_o + h * DH + 32 * c + lane] = __float2bfloat16(acc[c] * inv);
+  for (int c = 0; c < W; c += 2) dst[c / 2] = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
   if (lse != nullptr && lane == 0) lse[at] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
