@@ -63,7 +63,8 @@ struct RopeArgs {
   const uint64_t* phase;
   int d, rot;
   int sec1, sec2, sec3;  // first pair of axes 1, 2, 3
-  int rows_per_block;
+  int rows_per_block;    // a power of two; in the backward pass the queries' blocks',
+  int rows_per_block_k;  // and the keys'
   int lanes;             // lanes of a head (power of two)
   float scale, sin_sign, eps;
   float* partial;        // backward: [blocks, d] weight-gradient partials
@@ -342,7 +343,8 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
   const int blk = key ? blockIdx.x - a.blocks_q : blockIdx.x;
   const int nblk = key ? gridDim.x - a.blocks_q : a.blocks_q;
   const int u = threadIdx.x & (a.lanes - 1), slot = threadIdx.x / a.lanes;
-  const int step = kThreads / a.lanes / a.rows_per_block;
+  const int R = key ? a.rows_per_block_k : a.rows_per_block;
+  const int step = kThreads / a.lanes / R;
   const int row = slot / step, first = slot & (step - 1);  // neighbouring heads side by side
   const bool unit = u < a.d / (2 * V);
   const float c = s.norm == VDN_NORM_RMS ? 1.f / static_cast<float>(a.d) : 1.f;
@@ -358,14 +360,14 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
   }
   // one run of passes over the heads of the block's row groups, so that the
   // ring does not drain between groups
-  const int64_t groups = (a.rows + a.rows_per_block - 1) / a.rows_per_block;
+  const int64_t groups = (a.rows + R - 1) / R;
   const int64_t my_groups = blk < groups ? (groups - blk + nblk - 1) / nblk : 0;
   const int passes = (s.heads + step - 1) / step;
   const uint32_t mine = smem_u32(ring) + threadIdx.x * W * 4;
   int64_t fg = 0;  // the next fetch: group (of this block's), pass and stage
   int fk = 0, fs = 0;
   auto fetch = [&] {
-    const int64_t r = (blk + fg * nblk) * a.rows_per_block + row;
+    const int64_t r = (blk + fg * nblk) * R + row;
     const int h = fk * step + first;
     if (fg < my_groups && unit && r < a.rows && h < s.heads) {
       const int64_t off = static_cast<int64_t>(h) * a.d;
@@ -385,8 +387,8 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
   for (int k = 0; k < kBwdStages - 1; ++k) fetch();
   int stage = 0;
   for (int64_t group = 0; group < my_groups; ++group) {
-    const int64_t r0 = (blk + group * nblk) * a.rows_per_block;
-    const int n = static_cast<int>(min(static_cast<int64_t>(a.rows_per_block), a.rows - r0));
+    const int64_t r0 = (blk + group * nblk) * R;
+    const int n = static_cast<int>(min(static_cast<int64_t>(R), a.rows - r0));
     const bool live = unit && row < n;
     float4 turns[V / 2];
     if (a.rot > 0) {
@@ -590,6 +592,21 @@ int rows_per_block(int64_t rows, int lanes, int heads0, int heads1, int sms) {
   return best;
 }
 
+// Rows of a group in the backward pass: the fewest passes for the block with
+// the most groups, a group's turns and barriers counted as half a pass.
+int backward_rows(int64_t rows, int lanes, int heads, int blocks) {
+  const int slots = kThreads / lanes;
+  int best = 1;
+  int64_t least = int64_t(1) << 62;
+  for (int n = 1; n <= slots && n <= 16; n *= 2) {
+    const int step = slots / n;  // heads a pass
+    const int64_t groups = ((rows + n - 1) / n + blocks - 1) / blocks;
+    const int64_t cost = groups * (2 * ((heads + step - 1) / step) + 1);
+    if (cost < least) best = n, least = cost;
+  }
+  return best;
+}
+
 vdn_status launch_forward(RopeArgs& a, int dtype, int layout, cudaStream_t stream) {
   if (a.rows == 0) return VDN_OK;
   a.rows_per_block = rows_per_block(a.rows, a.lanes, a.s[0].heads, a.s[1].heads,
@@ -686,19 +703,20 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
                   ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes)
                   : nullptr;
   const int sms = sm_count_of_current_device();
-  a.rows_per_block = rows_per_block(rows, a.lanes, H, H_kv, sms);
-  // blocks shared out by heads; at most four an SM, at most one a row group
-  const int64_t groups = (rows + a.rows_per_block - 1) / a.rows_per_block;
-  const int most = 4 * sms < kMaxBwdBlocks ? 4 * sms : kMaxBwdBlocks - 1;  // each side has one
+  // two blocks an SM run at a time; shared out by heads, at most one a row
+  const int most = 2 * sms < kMaxBwdBlocks ? 2 * sms : kMaxBwdBlocks - 1;  // each side has one
   auto share = [&](int heads) {
     int64_t n = static_cast<int64_t>(most) * heads / (H + H_kv);
-    n = n > groups ? groups : n;
+    n = n > rows ? rows : n;
     return static_cast<int>(n < 1 ? 1 : n);
   };
   a.blocks_q = share(H);
   const int blocks = a.blocks_q + share(H_kv);
+  a.rows_per_block = backward_rows(rows, a.lanes, H, a.blocks_q);
+  a.rows_per_block_k = backward_rows(rows, a.lanes, H_kv, blocks - a.blocks_q);
   const int vec = vector_width(dtype, a.d, a.rot) * (dtype == VDN_DTYPE_F32 ? 4 : 2);
-  const int ring = kBwdStages * 4 * kThreads * vec + a.rows_per_block * a.rot / 2 * 8;
+  const int most_rows = a.rows_per_block > a.rows_per_block_k ? a.rows_per_block : a.rows_per_block_k;
+  const int ring = kBwdStages * 4 * kThreads * vec + most_rows * a.rot / 2 * 8;
   const int sums = kThreads / a.lanes * a.d * 4;
   const cudaError_t e = dispatch(
       dtype, vector_width(dtype, a.d, a.rot), plan->layout == VDN_ROPE_INTERLEAVED,

@@ -622,7 +622,7 @@ NORMS = {None: 0, "none": 0, "rms": 1, "l2": 2}
 def _same_device(*ts):
     """Every tensor on the current CUDA device (the kernels are launched
     there); returns its index."""
-    cur = torch.cuda.current_device()
+    cur = _current_device()
     for t in ts:
         if t is not None and t.get_device() != cur:
             _need_cuda(t)
@@ -630,8 +630,10 @@ def _same_device(*ts):
     return cur
 
 
-# The raw handle of the current stream without building a Stream object (the
-# calls below are short enough for its cost to show), where torch offers it.
+# The current device's index and the current stream's raw handle without the
+# objects around them (the calls below are short enough for their cost to
+# show), where torch offers it.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -652,6 +654,8 @@ def _mat(name, t, rows, cols, dtype):
     columns; one row or none has no stride of its own."""
     if t.dtype is not dtype or t.shape != (rows, cols):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, expected {dtype} [{rows}, {cols}]")
+    if t.is_contiguous():
+        return t.data_ptr(), cols
     if rows <= 1:
         if rows and cols > 1 and t.stride(1) != 1:
             raise ValueError(f"{name}: columns must be contiguous")
