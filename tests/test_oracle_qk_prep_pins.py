@@ -2,12 +2,14 @@
 a rotation: lengths kept, relative positions, the two layouts the same up to a
 permutation; and the plan's frequencies and fixed-point phases."""
 
+import ctypes
 import math
 
 import numpy as np
 import pytest
 
 from oracle import qk_prep
+from tests.parity_util import ensure_built
 from video_diffusion_hybrid_vda_b200 import vdn
 
 RNG = np.random.default_rng(5)
@@ -112,3 +114,77 @@ def test_bad_plans_are_refused():
                dict(frequencies=[float("nan")] * 8)):
         with pytest.raises(ValueError):
             vdn.RopePlan(16, device="cpu", **kw)
+
+
+# ---------------------------------------------------------------- refusals on the host
+
+A = 4096  # an aligned stand-in address; nothing reads it
+
+
+@pytest.fixture(scope="module")
+def L():
+    ensure_built()
+    return vdn
+
+
+def _plan(**kw):
+    base = dict(head_dim=64, rot_dim=32, layout=0, n_axes=1, section_pairs=(16, 0, 0, 0), scale=1.0,
+                phase=A)
+    base.update(kw)
+    pairs = (ctypes.c_int * 4)(*base["section_pairs"])
+    return vdn.RopePlanC(base["head_dim"], base["rot_dim"], base["layout"], base["n_axes"], pairs,
+                         base["scale"], base["phase"])
+
+
+BAD_PLANS = [
+    (dict(head_dim=0), 1), (dict(head_dim=60), 2), (dict(head_dim=264, rot_dim=0), 2),
+    (dict(rot_dim=-8), 1), (dict(rot_dim=72), 1), (dict(rot_dim=12), 2), (dict(layout=2), 1),
+    (dict(n_axes=0), 1), (dict(n_axes=5), 1), (dict(section_pairs=(15, 0, 0, 0)), 1),
+    (dict(n_axes=2, section_pairs=(17, -1, 0, 0)), 1), (dict(phase=0), 1), (dict(phase=A + 4), 1)]
+BAD_ARGS = [
+    (dict(dtype=3), 1), (dict(dtype=-1), 1), (dict(rows=-1), 1), (dict(rows=1 << 31), 1),
+    (dict(H=0), 1), (dict(x=0), 1), (dict(x=A + 8), 1), (dict(ld=120), 1), (dict(ld=132), 1),
+    (dict(out=0), 1), (dict(ld_out=64), 1), (dict(positions=A + 2), 1), (dict(rows=0, x=0), 0)]
+
+
+@pytest.mark.parametrize("plan,args,code", [(p, {}, c) for p, c in BAD_PLANS] +
+                         [({}, a, c) for a, c in BAD_ARGS])
+def test_rope_refuses_bad_arguments_on_the_host(L, plan, args, code):
+    lib, P = L.lib(), ctypes.c_void_p
+    a = dict(dtype=0, rows=10, H=2, x=A, ld=128, out=A, ld_out=128, positions=A)
+    a.update(args)
+    p = _plan(**plan)
+    assert lib.vdn_rope(ctypes.byref(p), a["dtype"], a["rows"], a["H"], P(a["x"]), a["ld"],
+                        P(a["positions"]), 10, 0, P(a["out"]), a["ld_out"], None) == code
+    assert lib.vdn_rope(None, 0, 10, 2, P(A), 128, None, 0, 0, P(A), 128, None) == 1
+
+
+def test_axes_need_a_stride_of_all_rows(L):
+    lib, P = L.lib(), ctypes.c_void_p
+    p = _plan(n_axes=2, section_pairs=(10, 6, 0, 0))
+    assert lib.vdn_rope(ctypes.byref(p), 0, 10, 2, P(A), 128, P(A), 9, 0, P(A), 128, None) == 1
+
+
+QK = dict(H=2, H_kv=1, q=A, ld_q=128, k=A, ld_k=64, q_norm=1, k_norm=2, wq=A, wk=0, eps=1e-6,
+          g=A, dq=A, dk=A, dwq=A, dwk=A, ws=A, ws_bytes=1 << 30)
+
+
+@pytest.mark.parametrize("change,code,forward", [
+    (dict(H_kv=0), 1, True), (dict(q=A + 8), 1, True), (dict(k=0), 1, True),
+    (dict(ld_k=60), 1, True), (dict(q_norm=3), 1, True), (dict(k_norm=-1), 1, True),
+    (dict(wq=A + 4), 1, True), (dict(q_norm=0), 1, True),      # a weight without a norm
+    (dict(eps=-1.0), 1, True), (dict(eps=float("nan")), 1, True), (dict(g=0), 1, False),
+    (dict(dq=0), 1, False), (dict(dk=A + 2), 1, False), (dict(dwq=A + 2), 1, False),
+    (dict(q_norm=0, wq=0), 1, False), (dict(ws=0), 3, False), (dict(ws=A + 16), 3, False),
+    (dict(ws_bytes=1000), 3, False)])
+def test_qk_norm_rope_refuses_bad_arguments_on_the_host(L, change, code, forward):
+    lib, P = L.lib(), ctypes.c_void_p
+    a = {**QK, **change}
+    p = _plan()
+    head = (ctypes.byref(p), 0, 10, a["H"], a["H_kv"], P(a["q"]), a["ld_q"], P(a["k"]), a["ld_k"],
+            a["q_norm"], a["k_norm"], P(a["wq"]), P(a["wk"]), a["eps"], None, 0)
+    if forward:
+        assert lib.vdn_qk_norm_rope(*head, P(A), 128, P(A), 64, None) == code
+    assert lib.vdn_qk_norm_rope_backward(
+        *head, P(a["g"]), 128, P(A), 64, P(a["dq"]), 128, P(a["dk"]), 64, P(a["dwq"]), P(a["dwk"]),
+        P(a["ws"]), a["ws_bytes"], None) == code

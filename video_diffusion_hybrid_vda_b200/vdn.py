@@ -875,7 +875,9 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
 _INT_MAX = (1 << 31) - 1
 
 
+@functools.lru_cache(maxsize=256)
 def _sink_shape(Lq, Lk, B, H, H_kv, d, window, sinks, ahead):
+    """The C shape (not to be changed: calls of the same sizes share it)."""
     window = _INT_MAX if window is None else min(int(window), _INT_MAX)
     return SinkShape(int(Lq), int(Lk), int(B), int(H), int(H_kv), int(d), window,
                      min(int(ahead), _INT_MAX), min(int(sinks), _INT_MAX))
@@ -1007,6 +1009,32 @@ def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, win
 
 # ---------------------------------------------------------------- full layer
 
+def video_positions(T, rows, cols, device=None):
+    """int32 [3, T*rows*cols]: frame, row and column of every token (frame-major,
+    then row-major), the positions of a three-axis RopePlan."""
+    n = rows * cols
+    i = torch.arange(T * n, dtype=torch.int32, device=device or "cuda")
+    return torch.stack([i // n, i % n // cols, i % cols])
+
+
+class QKPrep:
+    """What HybridLayer does to the projected queries and keys before its
+    branches: qk_norm_rope's arguments.  Keys of unit length ("l2") by default,
+    as Video Delta Attention takes them; ``positions`` for all T*N tokens
+    (video_positions), default the token's index."""
+
+    def __init__(self, plan, wq=None, wk=None, q_norm="rms", k_norm="l2", eps=1e-6,
+                 positions=None):
+        self.plan, self.wq, self.wk = plan, wq, wk
+        self.q_norm, self.k_norm, self.eps, self.positions = q_norm, k_norm, eps, positions
+
+    def __call__(self, q, k, H, q_out, k_out, stream=None):
+        """On H heads given as [T*N, H*d] (column views allowed, in place allowed)."""
+        return qk_norm_rope(q, k, H, H, self.plan, wq=self.wq, wk=self.wk, q_norm=self.q_norm,
+                            k_norm=self.k_norm, eps=self.eps, positions=self.positions,
+                            q_out=q_out, k_out=k_out, stream=stream)
+
+
 class HybridLayer:
     """The video-to-video hybrid attention layer on one GPU.
 
@@ -1019,12 +1047,15 @@ class HybridLayer:
     quantized once here, x on every call); ``softmax="mxfp8"`` runs the
     window Softmax with both products on MXFP8 operands (q, k, v quantized
     on every call; head dim 128, tokens per frame a multiple of 32).
+    ``qk_prep`` (a QKPrep) norms and rotates q and k of every call in one
+    more kernel before the branches; without it they are taken as given.
     """
 
     KERNELS_PER_FORWARD = 7   # prep, solve, scan, read-out, window Softmax, 2 GEMMs
 
     def __init__(self, T, N, H, d, W_gs, W_gl, W_os, W_ol, gamma, eps=1e-6, chunk_frames=5,
-                 window_chunks=1, anchors=3, device=None, projections="bf16", softmax="bf16"):
+                 window_chunks=1, anchors=3, device=None, projections="bf16", softmax="bf16",
+                 qk_prep=None):
         self.T, self.N, self.H, self.d = int(T), int(N), int(H), int(d)
         self.L, self.D = self.T * self.N, self.H * self.d
         self.device = torch.device(device or "cuda")
@@ -1058,6 +1089,13 @@ class HybridLayer:
             self.kernels_per_forward = self.KERNELS_PER_FORWARD
         if softmax == "mxfp8":
             self.kernels_per_forward += 3  # quantization of q, k, v
+        if qk_prep is not None and qk_prep.plan.d != self.d:
+            raise ValueError("qk_prep: a plan of the layer's head dim")
+        self.qk_prep = qk_prep
+        if qk_prep is not None:
+            self.kernels_per_forward += 1
+            self.qn = torch.empty((L, D), dtype=torch.bfloat16, device=dev)
+            self.kn = torch.empty((L, D), dtype=torch.bfloat16, device=dev)
         self._staging = None
 
     def _window_heads(self, q, k, v, hg, out, stream):
@@ -1108,6 +1146,10 @@ class HybridLayer:
         stream = stream or torch.cuda.current_stream(self.device)
         q, k, v, beta, alpha, x = self._to_device([q, k, v, beta, alpha, x], stream)
         T, N, H, d = self.T, self.N, self.H, self.d
+        if self.qk_prep is not None:  # the caller's q and k stay as they are
+            q, k = self.qk_prep(q, k, H, self.qn, self.kn, stream)
+            if v.stride(0) != q.stride(0):
+                v = v.contiguous()
         self._window(q, k, v, stream, ctx_k, ctx_v)
         vda_scan(q, k, v, beta, alpha, T, N, H, d, out=self.o_vda, ws=self.ws_vda, stream=stream)
         self._fuse(x, self.y, stream)
@@ -1233,11 +1275,15 @@ class HybridLayer:
                 for (h0, hg), (bg, ag), ev in zip(groups, self._grp_ba, grp_loaded):
                     stream.wait_event(ev)
                     c = slice(h0 * d, (h0 + hg) * d)
+                    if self.qk_prep is not None:
+                        self.qk_prep(q[:, c], k[:, c], hg, q[:, c], k[:, c], stream)
                     self._window_heads(q[:, c], k[:, c], v[:, c], hg, self.o_s[:, c], stream)
                     vda_scan(q[:, c], k[:, c], v[:, c], bg, ag, T, N, hg, d,
                              out=self.o_vda[:, c], ws=self.ws_vda, stream=stream)
             else:
                 stream.wait_event(loaded_qkv[i])
+                if self.qk_prep is not None:
+                    self.qk_prep(q, k, H, q, k, stream)
                 self._window(q, k, v, stream)
                 stream.wait_event(loaded[i])                    # beta, alpha, x
                 vda_scan(q, k, v, beta, alpha, T, N, H, d, out=self.o_vda, ws=self.ws_vda,
