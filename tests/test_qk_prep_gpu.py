@@ -248,6 +248,28 @@ def test_same_call_same_bits_in_place_and_captured(vdn):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("dtype,rot", [("bf16", 48), ("bf16", 40), ("fp32", 16)])
+def test_columns_past_the_rotated_ones_are_copied(vdn, layout, dtype, rot):
+    """Infinities and NaN there stay where they are, beside rotated columns too."""
+    plan = vdn.RopePlan(64, rot=rot, layout=layout)
+    gen = torch.Generator("cuda").manual_seed(1)
+    x = _wide(50, 128, DT[dtype], gen).view(50, 2, 64)
+    x[..., rot::3] = float("inf")
+    x[3, 1, rot + 1] = float("nan")
+    x = x.reshape(50, 128)
+    for inverse in (False, True):
+        y = vdn.rope(x, 2, plan, inverse=inverse).view(50, 2, 64)
+        assert torch.isfinite(y[..., :rot]).all()
+        same = torch.equal(y[..., rot:].nan_to_num(5.0, posinf=9.0),
+                           x.view(50, 2, 64)[..., rot:].nan_to_num(5.0, posinf=9.0))
+        assert same
+    g = torch.ones_like(x)
+    dq, _, _, _, _ = vdn.qk_norm_rope_backward(x, x, g, g, 2, 2, plan, q_norm="none",
+                                               k_norm="none")
+    assert torch.isfinite(dq).all()          # a rotation's gradient needs nothing of x
+
+
 def test_no_rows(vdn):
     plan = vdn.RopePlan(64)
     e = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")

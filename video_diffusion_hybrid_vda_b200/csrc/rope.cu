@@ -69,6 +69,7 @@ struct RopeArgs {
   float scale, sin_sign, eps;
   float* partial;        // backward: [blocks, d] weight-gradient partials
   int blocks_q;          // backward: blocks that work on queries (the rest on keys)
+  uint32_t* status;      // backward: device status word
 };
 
 template <int WORDS>
@@ -164,7 +165,7 @@ __device__ __forceinline__ void fill_turns(const RopeArgs& a, float2* cs, int64_
 // The turns of a unit's pairs in one row, (cos, sin, cos, sin) of two pairs a
 // float4: pair e of the half layout joins element e of both vectors; in the
 // interleaved layout the first V / 2 pairs lie in the vector at column ca, the
-// others in that at cb.  Columns past the rotated ones turn by nothing.
+// others in that at cb.
 template <int V, bool INTER>
 __device__ __forceinline__ void load_turns(const float2* cs, int rot, int ca, int cb,
                                            float4 (&c)[V / 2]) {
@@ -172,13 +173,15 @@ __device__ __forceinline__ void load_turns(const float2* cs, int rot, int ca, in
 #pragma unroll
   for (int j = 0; j < V / 2; ++j) {
     const int col = INTER ? (j < V / 4 ? ca + 4 * j : cb + 4 * j - V) : ca;
-    c[j] = make_float4(1.f, 0.f, 1.f, 0.f);
     if (col < (INTER ? rot : rot / 2)) c[j] = INTER ? p[col / 4] : p[ca / 2 + j];
   }
 }
 
+// `both`: the vector at cb turns too (in the half layout it always does); one
+// that passes through is left alone, since x * 1 - y * 0 is not x beside an
+// infinite y.
 template <int V, bool INTER>
-__device__ __forceinline__ void turn_unit(const float4 (&c)[V / 2], float (&fa)[V],
+__device__ __forceinline__ void turn_unit(const float4 (&c)[V / 2], bool both, float (&fa)[V],
                                           float (&fb)[V]) {
   auto turn = [](float& x, float& y, float cn, float sn) {
     const float t = x * cn - y * sn;
@@ -188,6 +191,7 @@ __device__ __forceinline__ void turn_unit(const float4 (&c)[V / 2], float (&fa)[
 #pragma unroll
   for (int j = 0; j < V / 2; ++j) {
     if constexpr (INTER) {
+      if (j >= V / 4 && !both) break;
       float(&f)[V] = j < V / 4 ? fa : fb;
       const int e = (4 * j) % V;
       turn(f[e], f[e + 1], c[j].x, c[j].y);
@@ -216,6 +220,16 @@ __device__ __forceinline__ void load_weight(const float* w, int col, float (&f)[
     const float4 v = *reinterpret_cast<const float4*>(w + col + e);
     f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
   }
+}
+
+// Both vectors' stores inside their tensor (debug builds; the forward calls
+// have no workspace to record a miss in and only skip it)?
+template <int V>
+__device__ __forceinline__ bool stores_in_bounds(const RopeArgs& a, const Side& s,
+                                                 uint32_t* status, int64_t r, int64_t c0,
+                                                 int64_t c1) {
+  const int64_t cols = static_cast<int64_t>(s.heads) * a.d;
+  return in_bounds(status, r, a.rows, c0, V, cols) && in_bounds(status, r, a.rows, c1, V, cols);
 }
 
 // Columns of unit u's two vectors: side by side with the neighbouring lanes'
@@ -250,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, NORM ? 3 : 4)
   const bool live = row < n && u < a.d / (2 * V);
   int ca, cb;
   unit_columns<V, INTER>(u, a.d, a.rot, ca, cb);
-  const bool turned = ca < (INTER ? a.rot : a.rot / 2);
+  const bool turned = ca < (INTER ? a.rot : a.rot / 2), both = !INTER || cb < a.rot;
   // passes over the heads of the queries, then of the keys
   const int passes_q = (a.s[0].heads + step - 1) / step;
   const int passes = passes_q + (a.s[1].heads + step - 1) / step;
@@ -316,11 +330,13 @@ __global__ void __launch_bounds__(kThreads, NORM ? 3 : 4)
       }
     }
     if (!on) continue;
-    if (turned) turn_unit<V, INTER>(turns, fa, fb);
+    if (turned) turn_unit<V, INTER>(turns, both, fa, fb);
     uint32_t oa[W], ob[W];
     pack<T, V, W>(fa, oa);
     pack<T, V, W>(fb, ob);
-    T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + static_cast<int64_t>(h) * a.d;
+    const int64_t col = static_cast<int64_t>(h) * a.d;
+    T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + col;
+    if (!stores_in_bounds<V>(a, s, nullptr, r0 + row, col + ca, col + cb)) continue;
     store_words<W>(dst + ca, oa);
     store_words<W>(dst + cb, ob);
   }
@@ -350,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
   const float c = s.norm == VDN_NORM_RMS ? 1.f / static_cast<float>(a.d) : 1.f;
   int ca, cb;
   unit_columns<V, INTER>(u, a.d, a.rot, ca, cb);
-  const bool turned = ca < (INTER ? a.rot : a.rot / 2);
+  const bool turned = ca < (INTER ? a.rot : a.rot / 2), both = !INTER || cb < a.rot;
   float wa[V], wb[V], da[V], db[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) wa[e] = wb[e] = 1.f, da[e] = db[e] = 0.f;
@@ -414,7 +430,7 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
         unpack<T, V, W>(v, fga);
         load_words<W>(src + 3 * SLOT, v);
         unpack<T, V, W>(v, fgb);
-        if (turned) turn_unit<V, INTER>(turns, fga, fgb);
+        if (turned) turn_unit<V, INTER>(turns, both, fga, fgb);
       } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) fxa[e] = fxb[e] = fga[e] = fgb[e] = 0.f;
@@ -440,13 +456,19 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(
           const float ra = r * fga[e], rb = r * fgb[e];
           da[e] += ra * fxa[e];
           db[e] += rb * fxb[e];
-          oa[e] = ra * wa[e] - fxa[e] * back;
-          ob[e] = rb * wb[e] - fxb[e] * back;
+          oa[e] = ra;
+          ob[e] = rb;
+          if (s.norm != VDN_NORM_NONE) {
+            oa[e] = ra * wa[e] - fxa[e] * back;
+            ob[e] = rb * wb[e] - fxb[e] * back;
+          }
         }
         uint32_t pa[W], pb[W];
         pack<T, V, W>(oa, pa);
         pack<T, V, W>(ob, pb);
-        T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + static_cast<int64_t>(h) * a.d;
+        const int64_t col = static_cast<int64_t>(h) * a.d;
+        T* dst = static_cast<T*>(s.y) + (r0 + row) * s.ldy + col;
+        if (!stores_in_bounds<V>(a, s, a.status, r0 + row, col + ca, col + cb)) continue;
         store_words<W>(dst + ca, pa);
         store_words<W>(dst + cb, pb);
       }
@@ -699,6 +721,7 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   a.eps = eps;
   a.sin_sign = -1.f;
+  a.status = static_cast<uint32_t*>(ws);
   a.partial = dwq || dwk
                   ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes)
                   : nullptr;

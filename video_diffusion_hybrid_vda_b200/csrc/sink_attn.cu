@@ -497,7 +497,8 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
                                                            const SinkOut parts,
                                                            __nv_bfloat16* __restrict__ o,
                                                            int64_t ld_o,
-                                                           float* __restrict__ lse) {
+                                                           float* __restrict__ lse,
+                                                           uint32_t* status) {
   constexpr int W = DH / 32;
   if (parts.zero_rest) sink_zero_rest(dims.cu_q, dims.B, dims.Lq, o, ld_o, dims.H * DH);
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
@@ -531,6 +532,9 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
     for (int c = 0; c < W; ++c) acc[c] += fs * x[c];
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (!in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH, DH,
+                 static_cast<int64_t>(dims.H) * DH))
+    return;
   uint32_t* dst = reinterpret_cast<uint32_t*>(o + static_cast<int64_t>(r) * ld_o + h * DH) +
                   W / 2 * lane;
 #pragma unroll
@@ -588,7 +592,7 @@ cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, const SinkCut& 
   if (splits > 1) {
     const int64_t warps = static_cast<int64_t>(dims.Lq) * dims.H;
     sink_combine_kernel<DH><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, ctx.stream>>>(
-        dims, splits, out, o, ld_o, lse);
+        dims, splits, out, o, ld_o, lse, ctx.status);
   }
   return cudaGetLastError();
 }

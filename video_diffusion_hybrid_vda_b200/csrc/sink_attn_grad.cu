@@ -726,7 +726,7 @@ __device__ __forceinline__ void sink_key_pass(int cta, const CUtensorMap& qmap,
 // the first inside the unit, if there is one.
 template <int DH>
 __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, const KeyPass a,
-                                                        float scale) {
+                                                        float scale, uint32_t* status) {
   const SinkPlan* p = a.plan;
   const int c1 = blockIdx.x + 1;
   if (c1 >= p->ctas) return;
@@ -753,8 +753,10 @@ __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, con
     x[4] += v.x, x[5] += v.y, x[6] += v.z, x[7] += v.w;
   }
   const float f = which ? scale : 1.f;
-  __nv_bfloat16* dst = (which ? a.dk : a.dv) +
-                       static_cast<int64_t>(seq.k0 + 128 * r.tile + row) * a.ld + hk * DH + c0;
+  const int64_t at_row = seq.k0 + 128 * r.tile + row;
+  if (!in_bounds(status, at_row, dims.Lk, hk * DH + c0, 8, static_cast<int64_t>(dims.Hkv) * DH))
+    return;
+  __nv_bfloat16* dst = (which ? a.dk : a.dv) + at_row * a.ld + hk * DH + c0;
   uint4 u;
   u.x = pack_bf16x2(x[0] * f, x[1] * f);
   u.y = pack_bf16x2(x[2] * f, x[3] * f);
@@ -1130,7 +1132,8 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
       t.q, t.d_o, t.k, t.v, dims, a, key_ctas, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
   if (cudaError_t e = cudaGetLastError()) return e;
   if (key_ctas > 1 && !st.whole)
-    sink_join_kernel<DH><<<dim3(key_ctas - 1, 16), 256, 0, ctx.stream>>>(dims, a, scale);
+    sink_join_kernel<DH><<<dim3(key_ctas - 1, 16), 256, 0, ctx.stream>>>(dims, a, scale,
+                                                                          ctx.status);
   return cudaGetLastError();
 }
 

@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kWarps * 32) sink_step_kernel(const StepArgs a
     const int ch = threadIdx.x % CH;
     __nv_bfloat16* dst = (v ? a.v_cache : a.k_cache) + b * a.batch_stride +
                          static_cast<int64_t>(slot) * a.ld_cache + hk * DH;
-    reinterpret_cast<uint4*>(dst)[ch] = reinterpret_cast<const uint4*>(v ? vn : kn)[ch];
+    // (no workspace: a debug build skips a miss without recording it)
+    if (in_bounds(nullptr, slot, slots, hk * DH + 8 * ch, 8, static_cast<int64_t>(a.Hkv) * DH))
+      reinterpret_cast<uint4*>(dst)[ch] = reinterpret_cast<const uint4*>(v ? vn : kn)[ch];
   }
 
   // Q as MMA rows (query heads g and g + 8 of this lane's quad)
@@ -297,8 +299,9 @@ __global__ void __launch_bounds__(kWarps * 32) sink_step_kernel(const StepArgs a
       sum += f * part_ml[k * 2 * kRows + kRows + r];
     }
     const float inv = 1.f / sum;
-    *reinterpret_cast<uint32_t*>(a.o + b * a.ld_o + (h0 + r) * DH + split * cols + c) =
-        pack_bf16x2(x * inv, y * inv);
+    const int col = (h0 + r) * DH + split * cols + c;
+    if (in_bounds(nullptr, b, gridDim.z, col, 2, static_cast<int64_t>(a.H) * DH))
+      *reinterpret_cast<uint32_t*>(a.o + b * a.ld_o + col) = pack_bf16x2(x * inv, y * inv);
   }
 }
 
