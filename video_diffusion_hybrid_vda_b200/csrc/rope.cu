@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, NORM ? 3 : 4)
 // columns) in registers; the block's sum goes to its row of `partial`, and
 // rope_dw_kernel adds the rows in a fixed order.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_backward_kernel(
+__global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(
     const __grid_constant__ RopeArgs a) {
   extern __shared__ float4 smem_f4[];
   constexpr int W = V * static_cast<int>(sizeof(T)) / 4;
@@ -726,7 +726,9 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
                   ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kStatusBytes)
                   : nullptr;
   const int sms = sm_count_of_current_device();
-  // two blocks an SM run at a time; shared out by heads, at most one a row
+  // two blocks an SM run at a time (125 registers at most; three, with 85, spill: 97 us
+  // for 10080 rows of 24 + 24 heads of 128 instead of 80; packed fp32
+  // arithmetic changes nothing); shared out by heads, at most one a row
   const int most = 2 * sms < kMaxBwdBlocks ? 2 * sms : kMaxBwdBlocks - 1;  // each side has one
   auto share = [&](int heads) {
     int64_t n = static_cast<int64_t>(most) * heads / (H + H_kv);
