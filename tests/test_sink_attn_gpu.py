@@ -163,6 +163,25 @@ def test_other_sequences_and_rows_of_none_do_not_reach_in(vdn):
     assert not fresh[:5].any() and not fresh[9:].any()
 
 
+@pytest.mark.parametrize("lead", [127, 128, 255, 256, 700])
+def test_rows_before_the_first_sequence(vdn, lead):
+    """Whole tiles of them, in front of queries and keys that look ahead."""
+    H, d, lens = 2, 64, [300, 77]
+    q, k, v, cq, ck = make(lens, lens, H, H, d, seed=lead)
+    kw = dict(window=90, sinks=4, ahead=400)
+    lse = torch.empty((H, sum(lens)), device="cuda")
+    ref = vdn.sink_attn(q, k, v, H, H, d, cu_q=cq, cu_k=ck, lse=lse, **kw)[0]
+    for lead_k in (0, lead):
+        qs, ks, vs = (torch.cat([torch.full((n, H * d), 5.0, device="cuda").bfloat16(), t])
+                      for n, t in ((lead, q), (lead_k, k), (lead_k, v)))
+        out, got = torch.full_like(qs, 9.0), torch.full((H, lead + sum(lens)), 9.0, device="cuda")
+        vdn.sink_attn(qs, ks, vs, H, H, d, cu_q=cq + lead, cu_k=ck + lead_k, out=out, lse=got, **kw)
+        assert torch.equal(out[lead:], ref) and torch.equal(got[:, lead:], lse)
+        assert (out[:lead] == 9).all() and (got[:, :lead] == 9).all()
+        fresh = vdn.sink_attn(qs, ks, vs, H, H, d, cu_q=cq + lead, cu_k=ck + lead_k, **kw)[0]
+        assert torch.equal(fresh[lead:], ref) and not fresh[:lead].any()
+
+
 def test_boundaries_outside_the_rows_are_clamped(vdn):
     q, k, v, _, _ = make([90], [90], 1, 1, 64)
     ref = vdn.sink_attn(q, k, v, 1, 1, 64, 33, 2)[0]

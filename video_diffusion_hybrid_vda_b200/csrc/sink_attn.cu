@@ -77,7 +77,7 @@ struct SinkUnit {
     const int b = sink_slot_seq(s.cu_q, s.B, s.Lq, c.rows, slot);
     const SinkSeq seq = sink_seq(s, b);
     const int at = c.rows * (slot - sink_slot_base(s.cu_q, b, s.Lq, c.rows));
-    if (at >= seq.nq()) return false;
+    if (at < 0 || at >= seq.nq()) return false;
     row0 = seq.q0 + at;
     row1 = seq.q1;
     h0 = in / c.splits * (256 / c.rows);

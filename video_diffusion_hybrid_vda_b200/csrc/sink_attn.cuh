@@ -61,8 +61,9 @@ __device__ __forceinline__ SinkSeq sink_seq(const SinkDims& s, int b) {
 // Tiles of packed sequences without a prefix sum over them: sequence b owns
 // the slots from cu[b] / tile + b on.  That is at least as many as it has
 // tiles (floor((c + n) / t) - floor(c / t) + 1 >= ceil(n / t)), so the grid
-// is L / tile + B slots, of which at most B have nothing to do, and a slot
-// finds its sequence by bisection over cu.
+// is L / tile + B slots, and a slot finds its sequence by bisection over cu.
+// Slots past a sequence's tiles have nothing to do, nor have those below the
+// first sequence's (a tile of rows or more before it): their tile is negative.
 __host__ __device__ __forceinline__ int sink_slots(int L, int B, int tile) {
   return L / tile + B;
 }

@@ -107,7 +107,7 @@ __device__ __forceinline__ SlotRec key_slot(const SinkDims& s, int slot) {
   const int tile = slot - sink_slot_base(s.cu_k, r.b, s.Lk, 128);
   const SinkSeq seq = sink_seq(s, r.b);
   const int ks = 128 * tile, nq = seq.nq(), shift = seq.shift();
-  if (ks >= seq.nk()) return r;  // a slot without a tile
+  if (tile < 0 || ks >= seq.nk()) return r;  // a slot without a tile
   const int ke = min(ks + 127, seq.nk() - 1);
   // queries [lo, hi) see a key of the tile
   const int lo = max(0, ks - shift - s.m.ahead);
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
   const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
   const SinkSeq seq = sink_seq(dims, b);
   const int tile0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
-  if (tile0 >= seq.q1) return;
+  if (tile0 < seq.q0 || tile0 >= seq.q1) return;
   const int lane = lane_id(), sub = lane / LANES, col = lane % LANES * 8;
   const int r0 = tile0 + first;
   for (int h = warp_id(); h < dims.H; h += 8) {
@@ -808,7 +808,7 @@ __device__ __forceinline__ void sink_query_pass(int cta, const CUtensorMap& qmap
   const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
   const SinkSeq seq = sink_seq(dims, b);
   const int row0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
-  if (row0 >= seq.q1) return;  // the whole CTA
+  if (row0 < seq.q0 || row0 >= seq.q1) return;  // the whole CTA
   const int pa = row0 - seq.q0 + seq.shift(), pb = min(pa + 127, seq.nk() - 1);
   SinkKeyTiles kt;
   kt.init(dims.m, pa, pb, seq.nk());
