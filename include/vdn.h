@@ -442,7 +442,8 @@ typedef struct {
  * x, out   : [rows, ld] of dtype; out may be x itself (same ld), and may not
  *            overlap it otherwise
  * positions: device int32, axis a's at positions + a * pos_stride, one a
- *            row; NULL: the row index on every axis
+ *            row (pos_stride 0: the same positions on every axis, else at
+ *            least rows); NULL: the row index on every axis
  * rows may be 0 (nothing is enqueued).  No workspace. */
 VDN_API vdn_status vdn_rope(const vdn_rope_plan* plan, int dtype, int64_t rows, int H,
                             const void* x, int64_t ld, const int32_t* positions,

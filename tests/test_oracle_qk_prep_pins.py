@@ -7,6 +7,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 from oracle import qk_prep
 from tests.parity_util import ensure_built
@@ -163,6 +164,18 @@ def test_axes_need_a_stride_of_all_rows(L):
     lib, P = L.lib(), ctypes.c_void_p
     p = _plan(n_axes=2, section_pairs=(10, 6, 0, 0))
     assert lib.vdn_rope(ctypes.byref(p), 0, 10, 2, P(A), 128, P(A), 9, 0, P(A), 128, None) == 1
+
+
+def test_stride_of_the_position_axes_is_the_tensors(L):
+    """Positions shared by the axes (stride 0) and columns of wider ones."""
+    plan = type("Plan", (), {"n_axes": 3})
+    pos = torch.arange(50, dtype=torch.int32)
+    for t, stride in ((pos.expand(3, 50), 0), (pos[:1].expand(3, 1), 0),
+                      (pos[:30].view(3, 10)[:, 4:9], 10), (pos[:30].view(3, 10)[:, 4:5], 10),
+                      (pos[:3].view(3, 1), 1)):
+        assert L._rope_positions(t, plan, t.shape[1]) == (t.data_ptr(), stride)
+    with pytest.raises(ValueError):
+        L._rope_positions(pos[:30].view(10, 3).t(), plan, 10)
 
 
 QK = dict(H=2, H_kv=1, q=A, ld_q=128, k=A, ld_k=64, q_norm=1, k_norm=2, wq=A, wk=0, eps=1e-6,

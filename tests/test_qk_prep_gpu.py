@@ -270,6 +270,17 @@ def test_columns_past_the_rotated_ones_are_copied(vdn, layout, dtype, rot):
     assert torch.isfinite(dq).all()          # a rotation's gradient needs nothing of x
 
 
+def test_positions_shared_by_the_axes(vdn):
+    plan = vdn.RopePlan(64, sections=[8, 8, 16])
+    x = torch.randn(37, 128, device="cuda").bfloat16()
+    one = torch.randint(0, 9000, (37,), device="cuda", dtype=torch.int32)
+    ref = vdn.rope(x, 2, plan, one.repeat(3, 1))
+    assert torch.equal(vdn.rope(x, 2, plan, one.expand(3, 37)), ref)
+    assert torch.equal(vdn.rope(x[:1], 2, plan, one[:1].expand(3, 1)), ref[:1])
+    with pytest.raises(vdn.VdnError):                   # axes that overlap
+        vdn.rope(x, 2, plan, torch.as_strided(one.repeat(3), (3, 37), (5, 1)))
+
+
 def test_no_rows(vdn):
     plan = vdn.RopePlan(64)
     e = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")

@@ -562,7 +562,8 @@ vdn_status take_plan(const vdn_rope_plan* plan, int64_t rows, const int32_t* pos
       sum += plan->section_pairs[i];
     }
     if (sum != plan->rot_dim / 2) return VDN_ERR_INVALID_ARG;
-    if (positions != nullptr && (!al(positions, 4) || (plan->n_axes > 1 && pos_stride < rows)))
+    if (positions != nullptr && (!al(positions, 4) ||
+                                 (plan->n_axes > 1 && pos_stride != 0 && pos_stride < rows)))
       return VDN_ERR_INVALID_ARG;
   }
   const int big = 1 << 30;

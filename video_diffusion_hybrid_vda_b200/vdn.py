@@ -786,7 +786,7 @@ def _rope_positions(positions, plan, rows):
         raise ValueError(f"positions: [{n}, {rows}]")
     if rows > 1 and positions.stride(-1) != 1:
         raise ValueError("positions: contiguous rows")
-    return positions.data_ptr(), max(positions.stride(0), rows) if n > 1 else rows
+    return positions.data_ptr(), positions.stride(0) if n > 1 else rows
 
 
 def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
