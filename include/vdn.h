@@ -510,9 +510,13 @@ VDN_API vdn_status vdn_qk_norm_rope_backward(
  * lse_opt: NULL, or fp32 [H, Lq]: natural-log sum of exp(scaled scores)
  * ws     : >= vdn_sink_attn_workspace(shape) bytes
  * Products run in bf16 with fp32 accumulation, P rounded to bf16 for the
- * product with V; sums and maxima in fp32.  A NaN or infinity in a key or
- * value that some query of a 128-query tile sees can reach the other queries
- * of that tile; rows of other sequences never do.
+ * product with V; sums and maxima in fp32.  Queries are taken in tiles of up
+ * to 256: a NaN or infinity in a key or value that one of a tile's queries
+ * sees can reach the others of the tile, and only those; rows of other
+ * sequences, or of none, never reach a sequence's results, not even their
+ * rounding.
+ * Calls that may run at the same time (other streams, graphs replayed side by
+ * side) need a workspace each, here and in the calls below.
  * ------------------------------------------------------------------------ */
 typedef struct {
   int Lq, Lk, B, H, H_kv, d;

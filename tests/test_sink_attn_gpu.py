@@ -163,6 +163,18 @@ def test_other_sequences_and_rows_of_none_do_not_reach_in(vdn):
     assert not fresh[:5].any() and not fresh[9:].any()
 
 
+def test_queries_behind_a_sequence_do_not_reach_its_roundings(vdn):
+    """Rows that share a tile with a sequence's last ones: their maxima grow
+    from key tile to key tile, and the sequence's bits stay."""
+    lens_q, lens_k, H, d = [100, 90], [900, 90], 2, 128
+    q, k, v, cq, ck = make(lens_q, lens_k, H, H, d, seed=8)
+    kw = dict(window=None, cu_q=cq, cu_k=ck)
+    ref = vdn.sink_attn(q, k, v, H, H, d, **kw)[0]
+    loud = q.clone()
+    loud[100:] *= 200
+    assert torch.equal(vdn.sink_attn(loud, k, v, H, H, d, **kw)[0][:100], ref[:100])
+
+
 @pytest.mark.parametrize("lead", [127, 128, 255, 256, 700])
 def test_rows_before_the_first_sequence(vdn, lead):
     """Whole tiles of them, in front of queries and keys that look ahead."""

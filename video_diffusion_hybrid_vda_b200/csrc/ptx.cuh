@@ -539,6 +539,21 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mas
       : "memory");
 }
 
+// ------------------------------------------------- launches that overlap
+
+// The kernel launched behind this one (launch_after) may be made resident as
+// soon as every block of this one has called this or ended.
+__device__ __forceinline__ void after_allow() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Wait until the kernels before this one have ended and what they wrote is
+// visible: the first thing that every thread of a kernel launched by
+// launch_after does.
+__device__ __forceinline__ void after_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ----------------------------------------------------------------- misc
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

@@ -354,6 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(
   constexpr int SLOT = kThreads * W * 4;  // bytes of one vector of all threads
   uint8_t* ring = reinterpret_cast<uint8_t*>(smem_f4);
   float2* cs = reinterpret_cast<float2*>(ring + kBwdStages * 4 * SLOT);
+  after_allow();  // rope_dw_kernel
   const bool key = static_cast<int>(blockIdx.x) >= a.blocks_q;
   const Side& s = a.s[key ? 1 : 0];
   const int blk = key ? blockIdx.x - a.blocks_q : blockIdx.x;
@@ -497,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(
 // columns, warp w every 32nd row from row w.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int d, int blocks_q,
                                                        int blocks, float* dwq, float* dwk) {
+  after_wait();
   __shared__ float sums[32][33];
   const bool key = blockIdx.y == 1;
   float* dw = key ? dwk : dwq;
@@ -757,9 +759,10 @@ vdn_status vdn_qk_norm_rope_backward(const vdn_rope_plan* plan, int dtype, int64
       });
   if (e != cudaSuccess) return VDN_ERR_CUDA;
   if (a.partial != nullptr) {
-    rope_dw_kernel<<<dim3((a.d + 31) / 32, 2), 1024, 0, st>>>(a.partial, a.d, a.blocks_q,
-                                                                blocks, dwq, dwk);
-    if (cudaGetLastError() != cudaSuccess) return VDN_ERR_CUDA;
+    if (launch_after(rope_dw_kernel, dim3((a.d + 31) / 32, 2), 1024, 0, st,
+                     static_cast<const float*>(a.partial), a.d, a.blocks_q, blocks, dwq, dwk) !=
+        cudaSuccess)
+      return VDN_ERR_CUDA;
   }
   return VDN_OK;
 }

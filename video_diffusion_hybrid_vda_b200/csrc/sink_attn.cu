@@ -119,6 +119,11 @@ __device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, const SinkUni
   const SinkMask m = dims.m;
   // this row's query and head within the unit, and its warp's first query
   const int query = (128 * i + row) & (cut.rows - 1), head = (128 * i + row) / cut.rows;
+  const int r = cur.row0 + query, h = cur.h0 + head;
+  // A maximum that has grown by less than this is kept: P stays below 2^8 and
+  // O is not rescaled for nothing.  Rows past the sequence never ask for it,
+  // so what they hold does not reach the other rows' roundings.
+  const float slack = r < cur.row1 ? 8.f : INFINITY;
   const int wq = (128 * i + quarter * 32) & (cut.rows - 1);
   const int warp_queries = min(32, cut.rows);
   const int p = cur.pa + query, pw = cur.pa + wq;
@@ -177,11 +182,9 @@ __device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, const SinkUni
     const float mt = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                            fmaxf(mx8[6], mx8[7])) *
                      scale_log2;
-    // The maximum in use moves only when some row's grew by more than 2^8
-    // (then P stays below 2^8 and O is not rescaled for nothing).  A row
-    // that has seen no key keeps -inf: its factor is 0 and its P below
-    // takes 0.
-    if (__any_sync(0xffffffffu, mt > m_used + 8.f)) {
+    // The maxima in use move when some row's has grown enough.  A row that
+    // has seen no key keeps -inf: its factor is 0 and its P below takes 0.
+    if (__any_sync(0xffffffffu, mt > m_used + slack)) {
       const float m_new = fmaxf(m_used, mt);
       const float factor = m_used == -INFINITY ? 0.f : exp2_mufu(m_used - m_new);
       l *= factor;
@@ -236,7 +239,6 @@ __device__ __forceinline__ bool sink_softmax(int i, uint32_t tmem, const SinkUni
   if (any && !__all_sync(0xffffffffu, mbar_wait(&o_done[i], (n - 1) & 1, budget_ns)))
     return false;
   tc_fence_after();
-  const int r = cur.row0 + query, h = cur.h0 + head;
   const bool live = r < cur.row1 && in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH,
                                               DH, static_cast<int64_t>(dims.H) * DH);
   const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: o = 0 (O holds no value if n == 0)
@@ -311,6 +313,7 @@ __global__ void __launch_bounds__(SinkCfg<DH>::THREADS, 1)
 
   if (out.zero_rest && out.o != nullptr)
     sink_zero_rest(dims.cu_q, dims.B, dims.Lq, out.o, out.ld_o, dims.H * DH);
+  after_allow();  // sink_combine_kernel, where there is one
   SinkUnit cur;
   if (!cur.init(dims, cut)) return;  // the whole CTA
   const uint32_t warp = warp_id();
@@ -500,6 +503,8 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
                                                            float* __restrict__ lse,
                                                            uint32_t* status) {
   constexpr int W = DH / 32;
+  constexpr int U = 16;  // parts whose loads are in flight before the first weight is known
+  after_wait();
   if (parts.zero_rest) sink_zero_rest(dims.cu_q, dims.B, dims.Lq, o, ld_o, dims.H * DH);
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
   const int r = static_cast<int>(w / dims.H), h = static_cast<int>(w % dims.H);
@@ -510,7 +515,14 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
   const int lane = lane_id();
   const int64_t at = static_cast<int64_t>(h) * dims.Lq + r;
   const int64_t step = static_cast<int64_t>(dims.H) * dims.Lq;
+  using Vec = std::conditional_t<W == 4, float4, float2>;
+  const Vec* src = reinterpret_cast<const Vec*>(
+                       parts.part_o + (static_cast<int64_t>(r) * dims.H + h) * DH) + lane;
   const float part = lane < splits ? parts.part_lse[lane * step + at] : -INFINITY;
+  Vec v[U];
+#pragma unroll
+  for (int s = 0; s < U; ++s)
+    if (s < splits) v[s] = src[s * step * 32];
   float top = part;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -519,18 +531,18 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
   float sum = f;
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  using Vec = std::conditional_t<W == 4, float4, float2>;
   float acc[W] = {};
-  const Vec* src = reinterpret_cast<const Vec*>(
-                       parts.part_o + (static_cast<int64_t>(r) * dims.H + h) * DH) + lane;
-#pragma unroll 8
-  for (int s = 0; s < splits; ++s) {
+  auto add = [&](int s, const Vec& u) {
     const float fs = __shfl_sync(0xffffffffu, f, s);
-    const Vec v = src[s * step * 32];
-    const float* x = reinterpret_cast<const float*>(&v);
+    const float* x = reinterpret_cast<const float*>(&u);
 #pragma unroll
     for (int c = 0; c < W; ++c) acc[c] += fs * x[c];
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < U; ++s)
+    if (s < splits) add(s, v[s]);
+#pragma unroll 8
+  for (int s = U; s < splits; ++s) add(s, src[s * step * 32]);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (!in_bounds(status, r, dims.Lq, static_cast<int64_t>(h) * DH, DH,
                  static_cast<int64_t>(dims.H) * DH))
@@ -591,8 +603,10 @@ cudaError_t launch_sink(const Launch& ctx, const SinkDims& dims, const SinkCut& 
   if (cudaError_t e = cudaGetLastError()) return e;
   if (splits > 1) {
     const int64_t warps = static_cast<int64_t>(dims.Lq) * dims.H;
-    sink_combine_kernel<DH><<<static_cast<unsigned>((warps + 7) / 8), 256, 0, ctx.stream>>>(
-        dims, splits, out, o, ld_o, lse, ctx.status);
+    if (cudaError_t e = launch_after(sink_combine_kernel<DH>,
+                                     dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0,
+                                     ctx.stream, dims, splits, out, o, ld_o, lse, ctx.status))
+      return e;
   }
   return cudaGetLastError();
 }

@@ -192,6 +192,7 @@ template <int DH>
 __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, const StatsArgs a) {
   constexpr int LANES = DH / 8, ROWS = 32 / LANES;  // rows a warp loads at once
   constexpr int U = 8;                              // loads in flight
+  after_allow();  // sink_grad_kernel
   if (dims.cu_q != nullptr) {
     if (a.zero[0] != nullptr)
       sink_zero_rest(dims.cu_q, dims.B, dims.Lq, a.zero[0], a.ld_zero[0], dims.H * DH);
@@ -727,6 +728,7 @@ __device__ __forceinline__ void sink_key_pass(int cta, const CUtensorMap& qmap,
 template <int DH>
 __global__ void __launch_bounds__(256) sink_join_kernel(const SinkDims dims, const KeyPass a,
                                                         float scale, uint32_t* status) {
+  after_wait();
   const SinkPlan* p = a.plan;
   const int c1 = blockIdx.x + 1;
   if (c1 >= p->ctas) return;
@@ -1065,6 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      const KeyPass a, int key_ctas, float scale, __nv_bfloat16* __restrict__ dq,
                      int64_t ld_dq, uint32_t* status, uint64_t budget_ns) {
   const int cta = blockIdx.x;
+  after_wait();
+  after_allow();  // sink_join_kernel, where there is one
   if (cta < key_ctas)
     sink_key_pass<DH>(cta, qmap, domap, kmap, vmap, dims, a, scale, status, budget_ns);
   else
@@ -1128,13 +1132,14 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
   sink_stats_kernel<DH><<<1 + 4 * q_slots, 256, 0, ctx.stream>>>(dims, st);
   if (cudaError_t e = cudaGetLastError()) return e;
   const int key_ctas = dims.Lk > 0 ? ctas : 0, query_ctas = dims.Lq > 0 ? q_slots * dims.H : 0;
-  sink_grad_kernel<DH><<<key_ctas + query_ctas, kThreads, Cfg::SMEM, ctx.stream>>>(
-      t.q, t.d_o, t.k, t.v, dims, a, key_ctas, scale, dq, ld_dq, ctx.status, ctx.budget_ns);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_after(sink_grad_kernel<DH>, dim3(key_ctas + query_ctas), kThreads,
+                                   Cfg::SMEM, ctx.stream, t.q, t.d_o, t.k, t.v, dims, a, key_ctas,
+                                   scale, dq, ld_dq, ctx.status, ctx.budget_ns))
+    return e;
   if (key_ctas > 1 && !st.whole)
-    sink_join_kernel<DH><<<dim3(key_ctas - 1, 16), 256, 0, ctx.stream>>>(dims, a, scale,
-                                                                          ctx.status);
-  return cudaGetLastError();
+    return launch_after(sink_join_kernel<DH>, dim3(key_ctas - 1, 16), 256, 0, ctx.stream, dims, a,
+                        scale, ctx.status);
+  return cudaSuccess;
 }
 
 }  // namespace
