@@ -107,6 +107,44 @@ def test_parity(vdn, lens_q, lens_k, H, Hkv, d, window, sinks, ahead, pad):
         assert torch.equal(x, y)                        # the same bits again
 
 
+@pytest.mark.parametrize("lens,d,window,sinks,ahead", [
+    ([700], 128, 2, 0, 0), ([700], 64, 3, 1, 0), ([900, 300], 128, 8, 2, 4), ([600], 64, 33, 4, 0),
+    ([16] * 40, 128, 1 << 30, 0, 0), ([50, 61, 3, 64] * 5, 64, 1 << 30, 0, 7),
+    ([500], 128, 20, 0, 100)])
+def test_few_keys_lose_nothing(vdn, lens, d, window, sinks, ahead):
+    """dq and dk of queries that see few keys are off by two roundings only,
+    dS's and their own: D_i = dO_i . o_i with the rounded o would be off by as
+    much again for all of a query's keys together.  A rounding's error is
+    uniform over a step, at most 2^-8 / sqrt(3) of its value in the mean square
+    (mantissa 1; less for others), and the errors add as squares, with 5 % for
+    the finite number of them.  The last case sees few keys in its first rows'
+    looks back and many ahead: its last rows alone see few."""
+    H = 2
+    q, k, v, cq, ck = make(lens, lens, H, H, d, seed=41)
+    g = make(lens, [0], H, 1, d, seed=42)[0]
+    out = step(vdn, q, k, v, g, H, H, d, window, sinks, ahead, cq, ck)
+    q, k, v, g, dq, dk = (_f64(x) for x in (q, k, v, g, out[0], out[1]))
+    err, ref, rounding, a = np.zeros(2), np.zeros(2), np.zeros(2), 0
+    for n in lens:
+        see, rows = visible(n, n, window, sinks, ahead), slice(a, a + n)
+        few = see.sum(1) <= 64
+        for h in range(H):
+            c = slice(h * d, (h + 1) * d)
+            qs, ks, vs, gs = (x[rows, c] for x in (q, k, v, g))
+            o, _, p = attend(qs, ks, vs, see, d ** -0.5)
+            ds = p * (gs @ vs.T - (gs * o).sum(1, keepdims=True)) * d ** -0.5
+            sides = [(dq[rows, c][few], (ds @ ks)[few], (ds * ds)[few] @ (ks * ks).sum(1))]
+            if few.all():
+                sides.append((dk[rows, c], ds.T @ qs, (ds * ds).T @ (qs * qs).sum(1)))
+            for i, (got, want, square) in enumerate(sides):
+                err[i] += ((got - want) ** 2).sum()
+                ref[i] += (want ** 2).sum()
+                rounding[i] += square.sum()
+        a += n
+    assert ref[0] > 0
+    assert (np.sqrt(err) <= 1.05 * H_ / 3 ** 0.5 * np.sqrt(ref + rounding)).all()
+
+
 def test_random_shapes(vdn):
     rng = np.random.default_rng(23)
     for _ in range(25):

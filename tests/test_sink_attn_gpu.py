@@ -245,6 +245,32 @@ def test_captured_replayed_and_on_another_stream(vdn):
         assert torch.equal(out, ref)
 
 
+def test_no_keys_at_all(vdn):
+    q, k, _, _, _ = make([300], [5], 4, 2, 64)
+    lse = torch.empty((4, 300), device="cuda")
+    o, ws = vdn.sink_attn(q, k[:0], k[:0], 4, 2, 64, 9, 2, 3, lse=lse)
+    assert not o.any() and (lse == -np.inf).all()
+    dq, dk, dv, ws2 = vdn.sink_attn_backward(q, k[:0], k[:0], o, lse, q, 4, 2, 64, 9, 2, 3)
+    assert not dq.any() and dk.shape == dv.shape == (0, 128)
+    assert vdn.get_device_status(ws) == vdn.get_device_status(ws2) == 0
+
+
+def test_two_calls_at_once(vdn):
+    """On two streams, with a workspace each (one call splits its keys)."""
+    jobs = []
+    for lens, lens_k, seed in (([2000], [2000], 1), ([30], [9000], 2)):
+        q, k, v, _, _ = make(lens, lens_k, 8, 2, 128, seed=seed)
+        ref, ws = vdn.sink_attn(q, k, v, 8, 2, 128, 5000, 4)
+        jobs.append((q, k, v, ref, ws, torch.empty_like(ref), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for q, k, v, _, ws, out, st in jobs:
+            vdn.sink_attn(q, k, v, 8, 2, 128, 5000, 4, out=out, ws=ws, stream=st)
+    torch.cuda.synchronize()
+    for _, _, _, ref, ws, out, _ in jobs:
+        assert torch.equal(out, ref) and vdn.get_device_status(ws) == 0
+
+
 def test_long_rows_against_sampled_queries(vdn):
     """20000 tokens, the oracle on a few queries of each kind."""
     n, H, Hkv, d, window, sinks = 20000, 8, 2, 128, 3000, 4

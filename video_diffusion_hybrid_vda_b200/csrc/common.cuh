@@ -84,10 +84,10 @@ cudaError_t set_smem_once(Kernel* kernel, int bytes, std::atomic<uint64_t>& done
   return e;
 }
 
-// Launch a kernel that begins with after_wait() (ptx.cuh) behind the one
-// before it on the stream: its blocks may become resident while the last of
-// the other's run (about half a microsecond a launch; 64 queries over 24000
-// keys and their join: 31.2 to 30.4 us in a graph).
+// Launch a kernel that calls after_wait() (ptx.cuh) behind the one before it on
+// the stream: its blocks may become resident while the last of the other's run
+// (about half a microsecond a launch; 64 queries over 24000 keys and their
+// join: 31.2 to 30.4 us in a graph).
 template <class Kernel, class... Args>
 cudaError_t launch_after(Kernel* kernel, dim3 grid, int block, int smem, cudaStream_t stream,
                          Args... args) {

@@ -539,6 +539,18 @@ __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mas
       : "memory");
 }
 
+// ------------------------------------------------------------ warp MMA
+
+// c += a b for one warp: a 16 x 16 (rows), b 16 x 8 (columns) bf16, c fp32.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // ------------------------------------------------- launches that overlap
 
 // The kernel launched behind this one (launch_after) may be made resident as
@@ -548,8 +560,8 @@ __device__ __forceinline__ void after_allow() {
 }
 
 // Wait until the kernels before this one have ended and what they wrote is
-// visible: the first thing that every thread of a kernel launched by
-// launch_after does.
+// visible.  Every thread of a kernel launched by launch_after calls it, before
+// it reads or overwrites anything of theirs.
 __device__ __forceinline__ void after_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }

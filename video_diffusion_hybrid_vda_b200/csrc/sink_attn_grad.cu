@@ -53,17 +53,33 @@ struct GradCfg {
 };
 
 // Per query, in tiles of 128 (the slots of sink_attn.cuh): -lse log2 e and
-// -D = -dO . o.  Rows past the sequence's end get -inf and 0: P = 0 there.
+// -D.  Rows past the sequence's end get -inf and 0: P = 0 there.
+// D = dO . o where a query sees many keys.  o is rounded, and made from a
+// rounded P, which puts D off by the same amount for all of a query's keys;
+// among few keys that weighs as much as all other roundings (2 keys: dq off by
+// 0.0042 of its norm in place of 0.0023; a window of 24: 0.0026, causal
+// sequences of up to some 500 tokens through their first queries alone: 0.0027
+// to 0.0026).  Groups of 16 queries whose first or last sees at most kFewKeys
+// keys therefore get D = sum_j P_ij (dO_i . v_j) from sink_few_kernel.
 // Rows of dq, dk and dv of no sequence are zeroed where asked.
 // A warp takes 32 rows of a head, DH / 8 lanes a row, so that lse is read and
 // both statistics are written 128 bytes at a time; the other heads' warps of
 // the block read the rest of the same rows.  Reading o and dO once is the whole
 // cost (a thread's rows in heads order, 4-byte accesses to [head][row] arrays:
 // 19.5 us for 8097 x 16 x 128, now 14.3).
+constexpr int kFewKeys = 64;
+constexpr int kFewRows = 16;  // the rows of a warp's MMA
+constexpr int kFewWarps = 4;  // that share a group and head's keys
+
 struct StatsArgs {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
   const __nv_bfloat16* o;
   const __nv_bfloat16* d_o;
-  int64_t ld_o, ld_do;
+  int64_t ld_q, ld_kv, ld_o, ld_do;
+  float scale_log2;
+  int few_blocks, few_stride;  // see sink_few_kernel
   const float* lse;
   float* nlse2;
   float* ndelta;
@@ -188,11 +204,138 @@ __device__ void make_plan(const SinkDims& s, const StatsArgs& a) {
     p->first[c] = x;
   }
 }
+
+// Keys that position p sees.
+__device__ __forceinline__ int sink_count(const SinkMask& m, int nk, int p) {
+  const int hi = min(nk, p + m.ahead + 1);
+  if (hi <= 0) return 0;
+  const int lo = max(0, p - m.window + 1), s = min(m.sinks, hi);
+  return lo <= s ? hi : hi - lo + s;
+}
+
+// Do the queries [row, row + kFewRows) of a sequence (row < nq) see few keys?
+__device__ __forceinline__ bool sink_few(const SinkMask& m, const SinkSeq& seq, int row) {
+  const int p0 = row + seq.shift(), p1 = min(row + kFewRows, seq.nq()) - 1 + seq.shift();
+  return min(sink_count(m, seq.nk(), p0), sink_count(m, seq.nk(), p1)) <= kFewKeys;
+}
+
+// D = sum_j P_ij (dO_i . v_j) of 16 queries and one head, over every
+// kFewWarps-th eight keys from the `part`-th on: S and dP by a warp's MMAs,
+// operands straight from memory (they are few).  Returns D of rows g and g + 8
+// in each quad g.
+template <int DH>
+__device__ __forceinline__ float2 sink_few_rows(const SinkDims& s, const StatsArgs& a,
+                                                const SinkSeq& seq, int row, int h, int part) {
+  const int lane = lane_id(), g = lane >> 2, c2 = 2 * (lane & 3), hk = h / (s.H / s.Hkv);
+  const int rows = min(kFewRows, seq.nq() - row), pa = row + seq.shift(), nk = seq.nk();
+  const __nv_bfloat16* q = a.q + static_cast<int64_t>(seq.q0 + row) * a.ld_q + h * DH + c2;
+  const __nv_bfloat16* w = a.d_o + static_cast<int64_t>(seq.q0 + row) * a.ld_do + h * DH + c2;
+  uint32_t qf[DH / 16][4], wf[DH / 16][4];
+#pragma unroll
+  for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int r = g + 8 * (f & 1), col = 16 * kk + 8 * (f >> 1);
+      const bool on = r < rows;
+      qf[kk][f] = on ? *reinterpret_cast<const uint32_t*>(q + r * a.ld_q + col) : 0u;
+      wf[kk][f] = on ? *reinterpret_cast<const uint32_t*>(w + r * a.ld_do + col) : 0u;
+    }
+  float nl[2], d[2] = {0.f, 0.f};  // of rows g and g + 8
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    nl[i] = g + 8 * i < rows ? a.lse[static_cast<int64_t>(h) * s.Lq + seq.q0 + row + g + 8 * i]
+                             : -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) nl[i] = nl[i] == -INFINITY ? -INFINITY : -nl[i] * 1.4426950408889634f;
+  SinkKeyTiles kt;
+  kt.init(s.m, pa, pa + rows - 1, nk);
+  const int n_sink = (kt.s_end + 7) / 8;  // eights of the sinks, then of the window
+  const int n = kt.n > 0 ? n_sink + (kt.hi - kt.w_lo + 7) / 8 : 0;
+  for (int t = part; t < n; t += kFewWarps) {
+    const int j0 = t < n_sink ? 8 * t : kt.w_lo + 8 * (t - n_sink);
+    const int end = t < n_sink ? kt.s_end : kt.hi;
+    const bool on = j0 + g < end;
+    const int64_t off = static_cast<int64_t>(seq.k0 + j0 + g) * a.ld_kv + hk * DH + c2;
+    uint32_t kf[DH / 16][2], vf[DH / 16][2];
+#pragma unroll
+    for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int64_t at = off + 16 * kk + 8 * f;
+        kf[kk][f] = on ? *reinterpret_cast<const uint32_t*>(a.k + at) : 0u;
+        vf[kk][f] = on ? *reinterpret_cast<const uint32_t*>(a.v + at) : 0u;
+      }
+    float sc[4] = {}, dp[4] = {};
+#pragma unroll
+    for (int kk = 0; kk < DH / 16; ++kk) {
+      mma16816(sc, qf[kk], kf[kk][0], kf[kk][1]);
+      mma16816(dp, wf[kk], vf[kk][0], vf[kk][1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = j0 + c2 + (e & 1), p = pa + g + 8 * (e >> 1);
+      const bool see = j < end && j <= p + s.m.ahead && (p - j < s.m.window || j < s.m.sinks);
+      if (see) d[e >> 1] += exp2_mufu(sc[e] * a.scale_log2 + nl[e >> 1]) * dp[e];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    d[i] += __shfl_xor_sync(0xffffffffu, d[i], 1);
+    d[i] += __shfl_xor_sync(0xffffffffu, d[i], 2);
+    if (nl[i] == -INFINITY) d[i] = 0.f;
+  }
+  return make_float2(d[0], d[1]);
+}
+
+// D of the groups with few keys, over the statistics kernel's: kFewWarps warps
+// a head, a block every few_stride-th group of a sequence.  With a window of
+// more than kFewKeys these are the groups that begin with a query whose look
+// ahead ends among the first kFewKeys keys, and all of a sequence of so few
+// keys.  Bound: the latency of a few dependent loads (8097 tokens in three
+// causal sequences, 16 heads of 128: 240 groups and heads, 8.5 us more in all;
+// as blocks of the statistics kernel, which then has more registers, 10 to 18).
+template <int DH>
+__global__ void __launch_bounds__(256, 2) sink_few_kernel(const SinkDims s, const StatsArgs a) {
+  after_allow();  // sink_grad_kernel
+  bool alone = false;  // the statistics kernel, whose D is overwritten, has ended
+  constexpr int HEADS = 8 / kFewWarps;
+  __shared__ float sums[8][kFewRows];
+  const int warp = warp_id(), lane = lane_id(), blocks = (s.H + HEADS - 1) / HEADS;
+  const int each = blocks * a.few_stride, slots = sink_slots(s.Lq, s.B, 128);
+  for (int64_t n = blockIdx.x; n < static_cast<int64_t>(s.B) * each; n += gridDim.x) {
+    const int b = static_cast<int>(n / each), i = static_cast<int>(n % each);
+    const int h = i % blocks * HEADS + warp / kFewWarps;
+    const SinkSeq seq = sink_seq(s, b);
+    const int end = s.m.window <= kFewKeys || seq.nk() <= kFewKeys
+                        ? seq.nq()
+                        : min(seq.nq(), kFewKeys - s.m.ahead - seq.shift());
+    for (int row = i / blocks * kFewRows; row < end; row += a.few_stride * kFewRows) {
+      if (!sink_few(s.m, seq, row)) continue;  // the whole block
+      if (h < s.H) {
+        const float2 d = sink_few_rows<DH>(s, a, seq, row, h, warp % kFewWarps);
+        if ((lane & 3) == 0) sums[warp][lane >> 2] = d.x, sums[warp][8 + (lane >> 2)] = d.y;
+      }
+      if (!alone) after_wait();
+      alone = true;
+      __syncthreads();
+      if (h < s.H && warp % kFewWarps == 0 && lane < kFewRows && row + lane < seq.nq()) {
+        const int64_t slot = sink_slot_base(s.cu_q, b, s.Lq, 128) + (row >> 7);
+        float d = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) d += sums[warp + w][lane];
+        a.ndelta[(h * static_cast<int64_t>(slots) + slot) * 128 + (row & 127) + lane] = -d;
+      }
+      __syncthreads();
+    }
+  }
+  if (!alone) after_wait();
+}
+
 template <int DH>
 __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, const StatsArgs a) {
+  after_allow();  // sink_few_kernel
   constexpr int LANES = DH / 8, ROWS = 32 / LANES;  // rows a warp loads at once
   constexpr int U = 8;                              // loads in flight
-  after_allow();  // sink_grad_kernel
   if (dims.cu_q != nullptr) {
     if (a.zero[0] != nullptr)
       sink_zero_rest(dims.cu_q, dims.B, dims.Lq, a.zero[0], a.ld_zero[0], dims.H * DH);
@@ -204,9 +347,9 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
     make_plan(dims, a);
     return;
   }
+  const int slots = sink_slots(dims.Lq, dims.B, 128);
   const int blk = blockIdx.x - 1;
   const int slot = blk >> 2, first = (blk & 3) * 32;
-  const int slots = sink_slots(dims.Lq, dims.B, 128);
   const int b = sink_slot_seq(dims.cu_q, dims.B, dims.Lq, 128, slot);
   const SinkSeq seq = sink_seq(dims, b);
   const int tile0 = seq.q0 + 128 * (slot - sink_slot_base(dims.cu_q, b, dims.Lq, 128));
@@ -1131,6 +1274,9 @@ cudaError_t launch_sink_grad(const Launch& ctx, const SinkDims& dims, const Grad
   const int q_slots = sink_slots(dims.Lq, dims.B, 128);
   sink_stats_kernel<DH><<<1 + 4 * q_slots, 256, 0, ctx.stream>>>(dims, st);
   if (cudaError_t e = cudaGetLastError()) return e;
+  if (cudaError_t e = launch_after(sink_few_kernel<DH>, dim3(st.few_blocks), 256, 0, ctx.stream,
+                                   dims, st))
+    return e;
   const int key_ctas = dims.Lk > 0 ? ctas : 0, query_ctas = dims.Lq > 0 ? q_slots * dims.H : 0;
   if (cudaError_t e = launch_after(sink_grad_kernel<DH>, dim3(key_ctas + query_ctas), kThreads,
                                    Cfg::SMEM, ctx.stream, t.q, t.d_o, t.k, t.v, dims, a, key_ctas,
@@ -1215,6 +1361,18 @@ vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const void* q, in
                    current_wait_budget_ns()};
   const float sc = scale > 0.f ? scale : 1.f / sqrtf(static_cast<float>(s.d));
   StatsArgs st{};
+  st.q = static_cast<const __nv_bfloat16*>(q);
+  st.k = static_cast<const __nv_bfloat16*>(k);
+  st.v = static_cast<const __nv_bfloat16*>(v);
+  st.ld_q = ld_q, st.ld_kv = ld_kv;
+  st.scale_log2 = sc * 1.4426950408889634f;
+  // groups of a sequence taken side by side: those of its beginning, or, where
+  // all may see few keys, as many as fill the GPU
+  const int64_t each = static_cast<int64_t>(s.B) * ((s.H * kFewWarps + 7) / 8);
+  int64_t side = kFewKeys / kFewRows + 1;
+  if (s.window <= kFewKeys) side = 4 * kCtas / each > 1 ? 4 * kCtas / each : 1;
+  st.few_stride = static_cast<int>(side);
+  st.few_blocks = static_cast<int>(each * side < (1 << 16) ? each * side : 1 << 16);
   st.o = static_cast<const __nv_bfloat16*>(o);
   st.d_o = static_cast<const __nv_bfloat16*>(d_o);
   st.ld_o = ld_o, st.ld_do = ld_do;
