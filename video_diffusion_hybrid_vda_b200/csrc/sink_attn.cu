@@ -26,6 +26,16 @@
 // Few queries leave most SMs without a unit: then the key tiles of each unit
 // are split over several, each writes its normalised part in fp32 with its
 // lse, and sink_combine_kernel joins them, o = sum_s e^(lse_s - lse) o_s.
+//
+// Bound: the chain score product -> softmax -> product with V of a row tile,
+// which the other row tile half hides (two S and two O accumulators fill TMEM
+// at d = 128).  16384 tokens, 16 heads over 4, window 4096: 430 to 460 us, 1.05
+// to 1.12 PFLOP/s of visible pairs (0.64 to 0.69 of the burst rate of a large
+// product, 0.76 to 0.82 of its sustained one); tensor and exponential pipes
+// each 40 % busy.  Also measured there: a quarter of the exponentials on the
+// FMA pipe 500 us, two warpgroups a row tile 513, key tiles of up to 64 valid
+// keys taken by halves 456 in place of 450 (and 15.4 in place of 16.2 us for
+// three short sequences).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -556,9 +566,11 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
 
 // Rows and splits of a unit, from the shape alone (the workspace depends on
 // them).  Heads share a unit where their queries fill it together: while a
-// sequence has on average no more queries than half the unit's.  Key tiles
-// are split only where units would leave half of 148 SMs idle, with four key
-// tiles (512 keys) at least a split.
+// sequence has on average no more queries than half the unit's (64 queries, 16
+// heads over 4, 24000 keys: 44 us with a unit a head, 27 with one for four).
+// Key tiles are split only where units would leave half of 148 SMs idle, with
+// four key tiles (512 keys) at least a split: the join takes 6 to 7 us, and a key
+// tile 1.9 of a CTA.
 SinkCut sink_cut(const vdn_sink_shape& s) {
   SinkCut c{256, 1};
   const int group = s.H / s.H_kv, mean = (s.Lq + s.B - 1) / s.B;

@@ -1200,7 +1200,16 @@ __device__ __forceinline__ void sink_query_pass(int cta, const CUtensorMap& qmap
 }
 
 // Both passes in one launch: they need nothing of each other, so the query
-// pass's tiles fill the SMs that the key pass has left.
+// pass's tiles fill the SMs that the key pass has left (three short sequences:
+// 41 to 25 us of kernels; 8097 tokens, 16 heads over 4, window 1024: 318 to 300).
+// Bound, as in the forward pass, by the chain of a tile: products, exponentials,
+// TMEM stores and loads, products; the tensor pipe is 42 % busy, the
+// exponentials' 25 %.  8097 tokens: 277 us, 0.70 PFLOP/s of the 14 d flop a
+// visible pair that the two passes do (10 d in one pass with atomic adds), 0.43
+// of the burst rate of a large product.  Measured and not kept: half the exponentials on the
+// FMA pipe (148 to 152 us key pass, 135 to 147 query pass); P^T through shared
+// memory in the key pass (271 to 273); query tiles dealt out like the key
+// pass's items (the same).
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     sink_grad_kernel(const __grid_constant__ CUtensorMap qmap,
@@ -1241,7 +1250,8 @@ GradLayout grad_layout(const vdn_sink_shape& s) {
   const double items = static_cast<double>(k_slots) * s.H *
                        (s.Lq / 128 + 2 + kUnitCost) / (2 * kUnitCost);
   l.ctas = items < 1 ? 1 : items > kCtas ? kCtas : static_cast<int>(items);
-  // Few and short units stay whole: at most one an SM, with 16 items at most
+  // Few and short units stay whole, which saves the join and a second load of
+  // the shared units' tiles: at most one an SM, with 16 items at most
   // (a query tile more at either end of what the window or the rows allow).
   const int64_t group = s.H / s.H_kv;
   int64_t tiles = s.Lq / 128 + 2;
