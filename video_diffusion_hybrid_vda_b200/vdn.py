@@ -666,6 +666,15 @@ def _mat(name, t, rows, cols, dtype):
     return t.data_ptr(), ld
 
 
+def _out(name, out, like, rows, cols):
+    """(out, its address, its row stride): a [rows, cols] result of `like`'s
+    dtype, a new one where none is given."""
+    if out is None:
+        out = like.new_empty((rows, cols))
+        return out, out.data_ptr(), cols
+    return (out, *_mat(name, out, rows, cols, like.dtype))
+
+
 def _vec(name, t, n):
     """Address of a contiguous fp32 [n] vector, or None."""
     if t is None:
@@ -800,9 +809,7 @@ def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
     if code is None:
         raise ValueError("rope: bf16, fp16 or fp32")
     xp, ld = _mat("x", x, rows, cols, dtype)
-    if out is None:
-        out = x.new_empty((rows, cols))
-    op, ld_out = _mat("out", out, rows, cols, dtype)
+    out, op, ld_out = _out("out", out, x, rows, cols)
     pos, stride = _rope_positions(positions, plan, rows)
     _check(lib().vdn_rope(plan._ref, code, rows, H, xp, ld, pos, stride, 1 if inverse else 0, op,
                           ld_out, _raw_stream(stream, dev)), "vdn_rope")
@@ -831,15 +838,11 @@ def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rm
     Returns (q_out, k_out)."""
     dev = _same_device(q, k, wq, wk, positions, q_out, k_out, plan.phase)
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
-    rows, dtype, d = q.shape[0], q.dtype, plan.d
-    if q_out is None:
-        q_out = q.new_empty((rows, H * d))
-    if k_out is None:
-        k_out = q.new_empty((rows, H_kv * d))
-    _check(lib().vdn_qk_norm_rope(
-        *args, *_mat("q_out", q_out, rows, H * d, dtype),
-        *_mat("k_out", k_out, rows, H_kv * d, dtype), _raw_stream(stream, dev)),
-        "vdn_qk_norm_rope")
+    rows, d = q.shape[0], plan.d
+    q_out, qp, ld_qo = _out("q_out", q_out, q, rows, H * d)
+    k_out, kp, ld_ko = _out("k_out", k_out, q, rows, H_kv * d)
+    _check(lib().vdn_qk_norm_rope(*args, qp, ld_qo, kp, ld_ko, _raw_stream(stream, dev)),
+           "vdn_qk_norm_rope")
     return q_out, k_out
 
 
@@ -852,10 +855,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
     dev = _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
     rows, dtype, d = q.shape[0], q.dtype, plan.d
-    if dq is None:
-        dq = q.new_empty((rows, H * d))
-    if dk is None:
-        dk = q.new_empty((rows, H_kv * d))
+    dq, dqp, ld_dq = _out("dq", dq, q, rows, H * d)
+    dk, dkp, ld_dk = _out("dk", dk, q, rows, H_kv * d)
     if dwq is None and NORMS[q_norm]:
         dwq = q.new_empty(d, dtype=torch.float32)
     if dwk is None and NORMS[k_norm]:
@@ -864,9 +865,8 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
         ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), q.device)
     _check(lib().vdn_qk_norm_rope_backward(
         *args, *_mat("dq_out", dq_out, rows, H * d, dtype),
-        *_mat("dk_out", dk_out, rows, H_kv * d, dtype), *_mat("dq", dq, rows, H * d, dtype),
-        *_mat("dk", dk, rows, H_kv * d, dtype), _vec("dwq", dwq, d), _vec("dwk", dwk, d),
-        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_qk_norm_rope_backward")
+        *_mat("dk_out", dk_out, rows, H_kv * d, dtype), dqp, ld_dq, dkp, ld_dk,
+        _vec("dwq", dwq, d), _vec("dwk", dwk, d), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
 
 
@@ -929,12 +929,11 @@ def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=Non
     shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
     Lq = shape.Lq
     new = out is None
-    if new:
-        out = q.new_empty((Lq, H * d))
+    out, op, ld_o = _out("out", out, q, Lq, H * d)
     if ws is None:
         ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(args[0])), q.device)
     _check(lib().vdn_sink_attn(
-        *args, *_mat("out", out, Lq, H * d, torch.bfloat16), 1 if new else 0,
+        *args, op, ld_o, 1 if new else 0,
         None if lse is None else _lse_addr(lse, H, Lq), ws.data_ptr(), ws.numel(),
         _raw_stream(stream, dev)), "vdn_sink_attn")
     return out, ws
@@ -954,22 +953,17 @@ def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=
     shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
     Lq, Lk, bf16 = shape.Lq, shape.Lk, torch.bfloat16
     new = (dq is None) | (dk is None) << 1 | (dv is None) << 2
-    if dq is None:
-        dq = q.new_empty((Lq, H * d))
-    if dk is None:
-        dk = q.new_empty((Lk, H_kv * d))
-    if dv is None:
-        dv = q.new_empty((Lk, H_kv * d))
-    dkp, ld_dkv = _mat("dk", dk, Lk, H_kv * d, bf16)
-    dvp, ld_dv = _mat("dv", dv, Lk, H_kv * d, bf16)
+    dq, dqp, ld_dq = _out("dq", dq, q, Lq, H * d)
+    dk, dkp, ld_dkv = _out("dk", dk, q, Lk, H_kv * d)
+    dv, dvp, ld_dv = _out("dv", dv, q, Lk, H_kv * d)
     if ld_dv != ld_dkv:
         raise ValueError("dk and dv must share one row stride")
     if ws is None:
         ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), q.device)
     _check(lib().vdn_sink_attn_backward(
         *args, *_mat("o", o, Lq, H * d, bf16), _lse_addr(lse, H, Lq),
-        *_mat("d_o", d_o, Lq, H * d, bf16), *_mat("dq", dq, Lq, H * d, bf16), dkp, dvp, ld_dkv,
-        new, ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_sink_attn_backward")
+        *_mat("d_o", d_o, Lq, H * d, bf16), dqp, ld_dq, dkp, dvp, ld_dkv, new,
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_sink_attn_backward")
     return dq, dk, dv, ws
 
 
@@ -997,12 +991,12 @@ def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, win
     if positions.dtype is not torch.int32 or positions.shape != (B,) or \
             not positions.is_contiguous():
         raise ValueError("positions: contiguous int32 [B]")
-    if out is None:
-        out = q.new_empty((B, H * d))
+    qp = _mat("q", q, B, H * d, bf16)
+    out, op, ld_o = _out("out", out, q, B, H * d)
     _check(lib().vdn_sink_attn_step(
-        B, H, H_kv, d, window, sinks, *_mat("q", q, B, H * d, bf16), knp, vnp, ld_new,
+        B, H, H_kv, d, window, sinks, *qp, knp, vnp, ld_new,
         k_cache.data_ptr(), v_cache.data_ptr(), strides[1] if shape[1] > 1 else shape[2],
-        strides[0], positions.data_ptr(), scale, *_mat("out", out, B, H * d, bf16),
+        strides[0], positions.data_ptr(), scale, op, ld_o,
         _raw_stream(stream, dev)), "vdn_sink_attn_step")
     return out
 
