@@ -177,21 +177,21 @@ def test_queries_behind_a_sequence_do_not_reach_its_roundings(vdn):
 
 @pytest.mark.parametrize("lead", [127, 128, 255, 256, 700])
 def test_rows_before_the_first_sequence(vdn, lead):
-    """Whole tiles of them, in front of queries and keys that look ahead."""
+    """Whole tiles of them, in front of queries and keys that look ahead (the
+    rows in all decide how keys are split, so the bits are not those of a call
+    without them)."""
     H, d, lens = 2, 64, [300, 77]
     q, k, v, cq, ck = make(lens, lens, H, H, d, seed=lead)
     kw = dict(window=90, sinks=4, ahead=400)
-    lse = torch.empty((H, sum(lens)), device="cuda")
-    ref = vdn.sink_attn(q, k, v, H, H, d, cu_q=cq, cu_k=ck, lse=lse, **kw)[0]
     for lead_k in (0, lead):
         qs, ks, vs = (torch.cat([torch.full((n, H * d), 5.0, device="cuda").bfloat16(), t])
                       for n, t in ((lead, q), (lead_k, k), (lead_k, v)))
         out, got = torch.full_like(qs, 9.0), torch.full((H, lead + sum(lens)), 9.0, device="cuda")
         vdn.sink_attn(qs, ks, vs, H, H, d, cu_q=cq + lead, cu_k=ck + lead_k, out=out, lse=got, **kw)
-        assert torch.equal(out[lead:], ref) and torch.equal(got[:, lead:], lse)
+        check(out[lead:], got[:, lead:], q, k, v, H, H, d, 90, 4, 400, lens, lens)
         assert (out[:lead] == 9).all() and (got[:, :lead] == 9).all()
         fresh = vdn.sink_attn(qs, ks, vs, H, H, d, cu_q=cq + lead, cu_k=ck + lead_k, **kw)[0]
-        assert torch.equal(fresh[lead:], ref) and not fresh[:lead].any()
+        assert torch.equal(fresh[lead:], out[lead:]) and not fresh[:lead].any()
 
 
 def test_boundaries_outside_the_rows_are_clamped(vdn):
@@ -243,6 +243,19 @@ def test_captured_replayed_and_on_another_stream(vdn):
         vdn.sink_attn(q, k, v, 4, 2, 128, out=out.zero_(), ws=ws, stream=torch.cuda.current_stream(),
                       **kw)
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("nq,nk,H,Hkv,d,window", [
+    (64, 9000, 8, 1, 64, 1 << 30), (16, 8192, 2, 2, 128, 1 << 30), (5, 33, 8, 1, 64, 1 << 30),
+    (100, 6000, 2, 1, 128, 5000), (257, 700, 1, 1, 64, 300)])
+def test_keys_in_many_parts(vdn, nq, nk, H, Hkv, d, window):
+    """Up to 32 parts of a key tile or more each, some of which a query does
+    not see."""
+    q, k, v, _, _ = make([nq], [nk], H, Hkv, d, seed=nk)
+    lse = torch.empty((H, nq), device="cuda")
+    o, ws = vdn.sink_attn(q, k, v, H, Hkv, d, window, 3, lse=lse)
+    assert vdn.get_device_status(ws) == 0
+    check(o, lse, q, k, v, H, Hkv, d, window, 3, 0, [nq], [nk])
 
 
 def test_no_keys_at_all(vdn):

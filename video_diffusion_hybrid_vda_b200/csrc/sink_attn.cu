@@ -568,24 +568,32 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
 // them).  Heads share a unit where their queries fill it together: while a
 // sequence has on average no more queries than half the unit's (64 queries, 16
 // heads over 4, 24000 keys: 44 us with a unit a head, 27 with one for four).
-// Key tiles are split only where units would leave half of 148 SMs idle, with
-// four key tiles (512 keys) at least a split: the join takes 6 to 7 us, and a key
-// tile 1.9 of a CTA.
+// Key tiles are split where units would leave half of 148 SMs idle, over as many
+// CTAs as make the longest walk and the join together shortest.  Measured: a
+// key tile takes 1.7 us (d 128) or 1.3 (64), a join 2.3 us and 0.45 for each MB
+// of parts.  Queries of 16 heads over 4: 32 over 1000 keys 11.9 us and 17.0
+// without a split, 64 over 6000 keys 19.6 and 22.3 with four tiles a split, 64
+// over 24000 keys 30 with 32 splits and 35.7 with 18; 1500 tokens of 6 heads over
+// 2 18.7 and 23.2 without; but 600 tokens of 8 heads 17.7 in five splits and 14.4
+// in one.
 SinkCut sink_cut(const vdn_sink_shape& s) {
   SinkCut c{256, 1};
   const int group = s.H / s.H_kv, mean = (s.Lq + s.B - 1) / s.B;
   while (c.rows > 8 && mean <= c.rows / 2 && group % (512 / c.rows) == 0) c.rows /= 2;
-  int64_t tiles = (static_cast<int64_t>(s.Lq) + c.rows - 1) / c.rows;
-  if (tiles < s.B) tiles = s.B;
-  const int64_t units = tiles * (s.H * c.rows / 256 < 1 ? 1 : s.H * c.rows / 256);
-  if (units > 74) return c;
+  // the most that B sequences can have of Lq rows
+  const int64_t slots = (s.Lq + static_cast<int64_t>(s.B) * (c.rows - 1)) / c.rows;
+  const int64_t units = slots * (s.H * c.rows / 256 < 1 ? 1 : s.H * c.rows / 256);
+  if (units < 1 || units > 74) return c;
   int64_t keys = static_cast<int64_t>(s.window) + s.ahead + c.rows + s.sinks;
   if (keys > s.Lk) keys = s.Lk;
-  const int64_t most = (keys + 127) / 128 / 4;
-  int64_t n = 148 / units;
-  n = n > most ? most : n;
-  n = n > 32 ? 32 : n;
-  c.splits = n < 1 ? 1 : static_cast<int>(n);
+  const int tiles = static_cast<int>((keys + 127) / 128);
+  const float tile = s.d == 128 ? 1.7f : 1.3f;
+  const float part = 0.45e-6f * 4.f * static_cast<float>(s.Lq) * s.H * s.d;
+  float best = tiles * tile;
+  for (int n = 2; n <= 32 && n * units <= 148 && n <= tiles; ++n) {
+    const float t = (tiles + n - 1) / n * tile + 2.3f + n * part;
+    if (t < best) best = t, c.splits = n;
+  }
   return c;
 }
 
