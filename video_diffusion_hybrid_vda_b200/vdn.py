@@ -1088,8 +1088,8 @@ class HybridLayer:
         self.qk_prep = qk_prep
         if qk_prep is not None:
             self.kernels_per_forward += 1
-            self.qn = torch.empty((L, D), dtype=torch.bfloat16, device=dev)
-            self.kn = torch.empty((L, D), dtype=torch.bfloat16, device=dev)
+            self._qk = {D: tuple(torch.empty((L, D), dtype=torch.bfloat16, device=dev)
+                                 for _ in range(2))}  # prepared q and k, by their row stride
         self._staging = None
 
     def _window_heads(self, q, k, v, hg, out, stream):
@@ -1134,16 +1134,41 @@ class HybridLayer:
                 dst.copy_(src, non_blocking=True)
         return self._staging
 
+    def _prepared(self, q, k, v, stream):
+        """(q, k) normed and rotated, and v, with one row stride, as the branches
+        take them.  The caller's q and k stay as they are: the results go to
+        buffers with v's row stride (the columns of a fused projection are read
+        where they stand), kept for each stride, since a captured call holds
+        their addresses.  A v that the branches cannot read (its stride or
+        address no multiple of 16 bytes, its columns apart) is copied, on
+        ``stream`` like all the rest."""
+        L, D, bf16 = self.L, self.D, torch.bfloat16
+        if v.dtype is not bf16 or v.numel() != L * D:
+            raise ValueError(f"v: {v.dtype} {tuple(v.shape)}, expected {bf16} [{L}, {D}]")
+        with torch.cuda.stream(stream):
+            v = v.reshape(L, D)
+            ld = v.stride(0)
+            if v.stride(1) != 1 or ld < D or ld % 8 or v.data_ptr() % 16:
+                v, ld = torch.empty((L, D), dtype=bf16, device=v.device).copy_(v), D
+            if ld not in self._qk:
+                if ld >= 2 * D:  # side by side in the same rows
+                    rows = torch.empty((L, ld), dtype=bf16, device=v.device)
+                    self._qk[ld] = rows[:, :D], rows[:, D:2 * D]
+                else:
+                    self._qk[ld] = tuple(torch.empty((L, ld), dtype=bf16, device=v.device)[:, :D]
+                                         for _ in range(2))
+        q, k = self.qk_prep(q, k, self.H, *self._qk[ld], stream)
+        return q, k, v
+
     def forward(self, q, k, v, beta, alpha, x, out=None, stream=None, ctx_k=None, ctx_v=None):
         """y for one video; ``ctx_k``/``ctx_v`` (CUDA, [M, D] bf16) are optional
-        text/audio keys the Softmax branch also attends to."""
+        text/audio keys the Softmax branch also attends to (taken as given, with
+        ``qk_prep`` too)."""
         stream = stream or torch.cuda.current_stream(self.device)
         q, k, v, beta, alpha, x = self._to_device([q, k, v, beta, alpha, x], stream)
         T, N, H, d = self.T, self.N, self.H, self.d
-        if self.qk_prep is not None:  # the caller's q and k stay as they are
-            q, k = self.qk_prep(q, k, H, self.qn, self.kn, stream)
-            if v.stride(0) != q.stride(0):
-                v = v.contiguous()
+        if self.qk_prep is not None:
+            q, k, v = self._prepared(q, k, v, stream)
         self._window(q, k, v, stream, ctx_k, ctx_v)
         vda_scan(q, k, v, beta, alpha, T, N, H, d, out=self.o_vda, ws=self.ws_vda, stream=stream)
         self._fuse(x, self.y, stream)
