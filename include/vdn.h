@@ -500,8 +500,8 @@ VDN_API vdn_status vdn_qk_norm_rope_backward(
  *          128 (VDN_ERR_UNSUPPORTED otherwise); window >= 1
  * q, o   : [Lq, ld] bf16;  k, v: [Lk, ld_kv] bf16
  * cu_q, cu_k: device int32 [B + 1], the first row of each sequence and the
- *          end of the last, ascending; NULL for one sequence of all rows
- *          (B = 1).  Rows that belong to no sequence (before the first, from
+ *          end of the last, ascending; either may be NULL with B = 1: the
+ *          one sequence has all of that side's rows.  Rows that belong to no sequence (before the first, from
  *          the last end on) never reach a result.  Values outside [0, L] are
  *          clamped.
  * zero_rest: 0: the rows of o and lse of no sequence stay as they are;

@@ -336,13 +336,13 @@ __global__ void __launch_bounds__(256) sink_stats_kernel(const SinkDims dims, co
   after_allow();  // sink_few_kernel
   constexpr int LANES = DH / 8, ROWS = 32 / LANES;  // rows a warp loads at once
   constexpr int U = 8;                              // loads in flight
-  if (dims.cu_q != nullptr) {
-    if (a.zero[0] != nullptr)
-      sink_zero_rest(dims.cu_q, dims.B, dims.Lq, a.zero[0], a.ld_zero[0], dims.H * DH);
+  // a side without offsets has no rows outside its one sequence
+  if (dims.cu_q != nullptr && a.zero[0] != nullptr)
+    sink_zero_rest(dims.cu_q, dims.B, dims.Lq, a.zero[0], a.ld_zero[0], dims.H * DH);
+  if (dims.cu_k != nullptr)
     for (int i = 1; i < 3; ++i)
       if (a.zero[i] != nullptr)
         sink_zero_rest(dims.cu_k, dims.B, dims.Lk, a.zero[i], a.ld_zero[i], dims.Hkv * DH);
-  }
   if (blockIdx.x == 0) {  // the other blocks have more to do
     make_plan(dims, a);
     return;
