@@ -4,6 +4,9 @@ Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  Tensors must live on the current CUDA device; PyTorch provides
 device memory and the stream.  If the library is missing, every call raises
 (there is no CPU fallback).
+
+A call that is given a ``stream`` runs there: the caller lets that stream wait
+for the inputs, and waits for it before reading the results.
 """
 
 import ctypes
@@ -242,11 +245,28 @@ def copy_columns_async(dst, dst_c0, src, src_c0, ncols, stream=None):
            "vdn_copy2d_async")
 
 
-def alloc_workspace(nbytes, device=None):
-    """Device workspace with a cleared status word."""
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8,
-                     device=device or torch.device("cuda"))
-    _check(lib().vdn_reset_device_status(_ptr(ws), _stream(None)), "vdn_reset_device_status")
+def _new(shape, dtype, device, stream):
+    """A new tensor for a call on ``stream``.  On a stream other than torch's
+    current one it is that stream's memory: the call comes after whatever used
+    the block before, and a tensor dropped while the call runs goes to nothing
+    but later work of the same stream.  Work on the current stream that reads
+    a result keeps it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if stream.cuda_stream == here.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def alloc_workspace(nbytes, device=None, stream=None):
+    """Device workspace with a cleared status word, for calls on ``stream``
+    (default: torch's current one)."""
+    ws = _new(max(int(nbytes), 256), torch.uint8, device or torch.device("cuda"), stream)
+    _check(lib().vdn_reset_device_status(_ptr(ws), _stream(stream)), "vdn_reset_device_status")
     return ws
 
 
@@ -666,11 +686,12 @@ def _mat(name, t, rows, cols, dtype):
     return t.data_ptr(), ld
 
 
-def _out(name, out, like, rows, cols):
+def _out(name, out, like, rows, cols, stream):
     """(out, its address, its row stride): a [rows, cols] result of `like`'s
     dtype, a new one where none is given."""
     if out is None:
-        out = like.new_empty((rows, cols))
+        out = like.new_empty((rows, cols)) if stream is None else \
+            _new((rows, cols), like.dtype, like.device, stream)
         return out, out.data_ptr(), cols
     return (out, *_mat(name, out, rows, cols, like.dtype))
 
@@ -809,7 +830,7 @@ def rope(x, H, plan, positions=None, inverse=False, out=None, stream=None):
     if code is None:
         raise ValueError("rope: bf16, fp16 or fp32")
     xp, ld = _mat("x", x, rows, cols, dtype)
-    out, op, ld_out = _out("out", out, x, rows, cols)
+    out, op, ld_out = _out("out", out, x, rows, cols, stream)
     pos, stride = _rope_positions(positions, plan, rows)
     _check(lib().vdn_rope(plan._ref, code, rows, H, xp, ld, pos, stride, 1 if inverse else 0, op,
                           ld_out, _raw_stream(stream, dev)), "vdn_rope")
@@ -839,8 +860,8 @@ def qk_norm_rope(q, k, H, H_kv, plan, wq=None, wk=None, q_norm="rms", k_norm="rm
     dev = _same_device(q, k, wq, wk, positions, q_out, k_out, plan.phase)
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
     rows, d = q.shape[0], plan.d
-    q_out, qp, ld_qo = _out("q_out", q_out, q, rows, H * d)
-    k_out, kp, ld_ko = _out("k_out", k_out, q, rows, H_kv * d)
+    q_out, qp, ld_qo = _out("q_out", q_out, q, rows, H * d, stream)
+    k_out, kp, ld_ko = _out("k_out", k_out, q, rows, H_kv * d, stream)
     _check(lib().vdn_qk_norm_rope(*args, qp, ld_qo, kp, ld_ko, _raw_stream(stream, dev)),
            "vdn_qk_norm_rope")
     return q_out, k_out
@@ -855,18 +876,19 @@ def qk_norm_rope_backward(q, k, dq_out, dk_out, H, H_kv, plan, wq=None, wk=None,
     dev = _same_device(q, k, dq_out, dk_out, wq, wk, positions, dq, dk, dwq, dwk, ws, plan.phase)
     args = _qk_args(q, k, H, H_kv, plan, wq, wk, q_norm, k_norm, eps, positions)
     rows, dtype, d = q.shape[0], q.dtype, plan.d
-    dq, dqp, ld_dq = _out("dq", dq, q, rows, H * d)
-    dk, dkp, ld_dk = _out("dk", dk, q, rows, H_kv * d)
+    dq, dqp, ld_dq = _out("dq", dq, q, rows, H * d, stream)
+    dk, dkp, ld_dk = _out("dk", dk, q, rows, H_kv * d, stream)
     if dwq is None and NORMS[q_norm]:
-        dwq = q.new_empty(d, dtype=torch.float32)
+        dwq = _new(d, torch.float32, q.device, stream)
     if dwk is None and NORMS[k_norm]:
-        dwk = q.new_empty(d, dtype=torch.float32)
+        dwk = _new(d, torch.float32, q.device, stream)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), q.device)
+        ws = alloc_workspace(int(lib().vdn_qk_norm_rope_backward_workspace(d)), q.device, stream)
     _check(lib().vdn_qk_norm_rope_backward(
         *args, *_mat("dq_out", dq_out, rows, H * d, dtype),
         *_mat("dk_out", dk_out, rows, H_kv * d, dtype), dqp, ld_dq, dkp, ld_dk,
-        _vec("dwq", dwq, d), _vec("dwk", dwk, d), ws.data_ptr(), ws.numel(), _raw_stream(stream, dev)), "vdn_qk_norm_rope_backward")
+        _vec("dwq", dwq, d), _vec("dwk", dwk, d), ws.data_ptr(), ws.numel(),
+        _raw_stream(stream, dev)), "vdn_qk_norm_rope_backward")
     return dq, dk, dwq, dwk, ws
 
 
@@ -929,9 +951,9 @@ def sink_attn(q, k, v, H, H_kv, d, window, sinks=0, ahead=0, cu_q=None, cu_k=Non
     shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
     Lq = shape.Lq
     new = out is None
-    out, op, ld_o = _out("out", out, q, Lq, H * d)
+    out, op, ld_o = _out("out", out, q, Lq, H * d, stream)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(args[0])), q.device)
+        ws = alloc_workspace(int(lib().vdn_sink_attn_workspace(args[0])), q.device, stream)
     _check(lib().vdn_sink_attn(
         *args, op, ld_o, 1 if new else 0,
         None if lse is None else _lse_addr(lse, H, Lq), ws.data_ptr(), ws.numel(),
@@ -953,13 +975,14 @@ def sink_attn_backward(q, k, v, o, lse, d_o, H, H_kv, d, window, sinks=0, ahead=
     shape, args = _sink_args(q, k, v, H, H_kv, d, window, sinks, ahead, cu_q, cu_k, scale)
     Lq, Lk, bf16 = shape.Lq, shape.Lk, torch.bfloat16
     new = (dq is None) | (dk is None) << 1 | (dv is None) << 2
-    dq, dqp, ld_dq = _out("dq", dq, q, Lq, H * d)
-    dk, dkp, ld_dkv = _out("dk", dk, q, Lk, H_kv * d)
-    dv, dvp, ld_dv = _out("dv", dv, q, Lk, H_kv * d)
+    dq, dqp, ld_dq = _out("dq", dq, q, Lq, H * d, stream)
+    dk, dkp, ld_dkv = _out("dk", dk, q, Lk, H_kv * d, stream)
+    dv, dvp, ld_dv = _out("dv", dv, q, Lk, H_kv * d, stream)
     if ld_dv != ld_dkv:
         raise ValueError("dk and dv must share one row stride")
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), q.device)
+        ws = alloc_workspace(int(lib().vdn_sink_attn_backward_workspace(args[0])), q.device,
+                             stream)
     _check(lib().vdn_sink_attn_backward(
         *args, *_mat("o", o, Lq, H * d, bf16), _lse_addr(lse, H, Lq),
         *_mat("d_o", d_o, Lq, H * d, bf16), dqp, ld_dq, dkp, dvp, ld_dkv, new,
@@ -992,7 +1015,7 @@ def sink_attn_step(q, k_new, v_new, k_cache, v_cache, positions, H, H_kv, d, win
             not positions.is_contiguous():
         raise ValueError("positions: contiguous int32 [B]")
     qp = _mat("q", q, B, H * d, bf16)
-    out, op, ld_o = _out("out", out, q, B, H * d)
+    out, op, ld_o = _out("out", out, q, B, H * d, stream)
     _check(lib().vdn_sink_attn_step(
         B, H, H_kv, d, window, sinks, *qp, knp, vnp, ld_new,
         k_cache.data_ptr(), v_cache.data_ptr(), strides[1] if shape[1] > 1 else shape[2],
