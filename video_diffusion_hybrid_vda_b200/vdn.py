@@ -245,19 +245,22 @@ def copy_columns_async(dst, dst_c0, src, src_c0, ncols, stream=None):
            "vdn_copy2d_async")
 
 
-def _new(shape, dtype, device, stream):
-    """A new tensor for a call on ``stream``.  On a stream other than torch's
-    current one it is that stream's memory: the call comes after whatever used
-    the block before, and a tensor dropped while the call runs goes to nothing
-    but later work of the same stream.  Work on the current stream that reads
-    a result keeps it too."""
+def _new(shape, dtype, device, stream, like=None):
+    """A new tensor for a call on ``stream`` (strided as ``like``, if given).
+    On a stream other than torch's current one it is that stream's memory: the
+    call comes after whatever used the block before, and a tensor dropped while
+    the call runs goes to nothing but later work of the same stream.  Work on
+    the current stream that reads a result keeps it too."""
+    def make():
+        return torch.empty(shape, dtype=dtype, device=device) if like is None else \
+            torch.empty_like(like)
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make()
     here = torch.cuda.current_stream(device)
     if stream.cuda_stream == here.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make()
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = make()
     t.record_stream(here)
     return t
 
@@ -305,7 +308,7 @@ def selftest_bounds(ws, r, rows, c, width, cols, stream=None):
 def selftest_exp2(x, stream=None):
     """(y_fma, y_mufu): the Softmax's two exponential paths on fp32 CUDA x."""
     _need_cuda(x)
-    y_fma, y_mufu = torch.empty_like(x), torch.empty_like(x)
+    y_fma, y_mufu = (_new(x.shape, x.dtype, x.device, stream, like=x) for _ in range(2))
     _check(lib().vdn_selftest_exp2(_ptr(x), _ptr(y_fma), _ptr(y_mufu), x.numel(),
                                    _stream(stream)), "vdn_selftest_exp2")
     return y_fma, y_mufu
@@ -327,9 +330,9 @@ def vda_scan(q, k, v, beta, alpha, T, N, H, d, out=None, states=None, ws=None, s
     _need_cuda(q, k, v, beta, alpha, out, states, ws)
     shape = _shape(T, N, H, d)
     if out is None:
-        out = torch.empty((T * N, H * d), dtype=torch.bfloat16, device=q.device)
+        out = _new((T * N, H * d), torch.bfloat16, q.device, stream)
     if ws is None:
-        ws = alloc_workspace(vda_scan_workspace(T, N, H, d), q.device)
+        ws = alloc_workspace(vda_scan_workspace(T, N, H, d), q.device, stream)
     code = lib().vdn_vda_scan(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), q.stride(0),
                               _ptr(beta), _ptr(alpha), _ptr(out), out.stride(0), _ptr(states),
                               _ptr(ws), ws.numel(), _stream(stream))
@@ -347,9 +350,9 @@ def vda_scan_static(q, k, v, beta, alpha, T, N, H, d, out=None, states=None, sta
     _need_cuda(q, k, v, beta, alpha, out, states, status)
     shape = _shape(T, N, H, d)
     if out is None:
-        out = torch.empty((T * N, H * d), dtype=torch.bfloat16, device=q.device)
+        out = _new((T * N, H * d), torch.bfloat16, q.device, stream)
     if status is None:
-        status = torch.zeros(1, dtype=torch.int32, device=q.device)
+        status = _new(1, torch.int32, q.device, stream)  # written by the call
     code = lib().vdn_vda_scan_static(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), q.stride(0),
                                      _ptr(beta), _ptr(alpha), _ptr(out), out.stride(0),
                                      _ptr(states), _ptr(status), _stream(stream))
@@ -388,15 +391,15 @@ def vda_backward(q, k, v, beta, alpha, d_o, T, N, H, d, dq=None, dk=None, dv=Non
     shape = _shape(T, N, H, d)
     dev = q.device
     L, D = T * N, H * d
-    dq = torch.empty((L, D), dtype=torch.bfloat16, device=dev) if dq is None else dq
-    dk = torch.empty((L, D), dtype=torch.bfloat16, device=dev) if dk is None else dk
-    dv = torch.empty((L, D), dtype=torch.bfloat16, device=dev) if dv is None else dv
+    dq = _new((L, D), torch.bfloat16, dev, stream) if dq is None else dq
+    dk = _new((L, D), torch.bfloat16, dev, stream) if dk is None else dk
+    dv = _new((L, D), torch.bfloat16, dev, stream) if dv is None else dv
     if not (dq.stride(0) == dk.stride(0) == dv.stride(0)):
         raise ValueError("dq, dk and dv must share one row stride")
-    dbeta = torch.empty((L, H), dtype=torch.float32, device=dev) if dbeta is None else dbeta
-    dalpha = torch.empty((T, H), dtype=torch.float32, device=dev) if dalpha is None else dalpha
+    dbeta = _new((L, H), torch.float32, dev, stream) if dbeta is None else dbeta
+    dalpha = _new((T, H), torch.float32, dev, stream) if dalpha is None else dalpha
     if ws is None:
-        ws = alloc_workspace(vda_backward_workspace(T, N, H, d), dev)
+        ws = alloc_workspace(vda_backward_workspace(T, N, H, d), dev, stream)
     code = lib().vdn_vda_backward(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), q.stride(0),
                                   _ptr(beta), _ptr(alpha), _ptr(d_o), d_o.stride(0), _ptr(dq),
                                   _ptr(dk), _ptr(dv), dq.stride(0), _ptr(dbeta), _ptr(dalpha),
@@ -435,8 +438,8 @@ def mxfp8_quantize(x, stream=None):
     bytes uint8 in the GEMM's tile layout)."""
     _need_cuda(x)
     R, K = x.shape
-    q = torch.empty((R, K), dtype=torch.uint8, device=x.device)
-    sf = torch.empty(max(mxfp8_scale_bytes(R, K), 16), dtype=torch.uint8, device=x.device)
+    q = _new((R, K), torch.uint8, x.device, stream)
+    sf = _new(max(mxfp8_scale_bytes(R, K), 16), torch.uint8, x.device, stream)
     _check(lib().vdn_mxfp8_quantize(_ptr(x), R, K, x.stride(0), _ptr(q), _ptr(sf), _stream(stream)),
            "vdn_mxfp8_quantize")
     return q, sf
@@ -448,9 +451,9 @@ def gemm_mxfp8(a, b, out_f32=False, ws=None, stream=None):
     _need_cuda(aq, asf, bq, bsf)
     M, K = aq.shape
     N = bq.shape[0]
-    c = torch.empty((M, N), dtype=torch.float32 if out_f32 else torch.bfloat16, device=aq.device)
+    c = _new((M, N), torch.float32 if out_f32 else torch.bfloat16, aq.device, stream)
     if ws is None:
-        ws = alloc_workspace(256, aq.device)
+        ws = alloc_workspace(256, aq.device, stream)
     _check(lib().vdn_gemm_mxfp8(M, N, K, _ptr(aq), _ptr(asf), _ptr(bq), _ptr(bsf), _ptr(c),
                                 int(bool(out_f32)), _ptr(ws), ws.numel(), _stream(stream)),
            "vdn_gemm_mxfp8")
@@ -460,9 +463,10 @@ def gemm_mxfp8(a, b, out_f32=False, ws=None, stream=None):
 def mxfp8_fuse_weights(W_gs, W_gl, W_os, W_ol, stream=None):
     """MXFP8 weights of the fuse: the stacked gate weights [W_gs; W_gl] and
     the side-by-side output weights [W_os | W_ol], each (codes, scales)."""
-    wg = mxfp8_quantize(torch.cat([W_gs, W_gl], dim=0).contiguous(), stream)
-    wo = mxfp8_quantize(torch.cat([W_os, W_ol], dim=1).contiguous(), stream)
-    return wg, wo
+    with torch.cuda.stream(stream):  # the copies too
+        wg = torch.cat([W_gs, W_gl], dim=0).contiguous()
+        wo = torch.cat([W_os, W_ol], dim=1).contiguous()
+    return mxfp8_quantize(wg, stream), mxfp8_quantize(wo, stream)
 
 
 def hybrid_fuse_mxfp8(x, o_s, o_vda, wg, gamma, wo, H, eps=1e-6, out=None, ws=None, stream=None):
@@ -471,9 +475,10 @@ def hybrid_fuse_mxfp8(x, o_s, o_vda, wg, gamma, wo, H, eps=1e-6, out=None, ws=No
     _need_cuda(x, o_s, o_vda, gamma, out, ws)
     L, D = x.shape
     if out is None:
-        out = torch.empty((L, D), dtype=torch.bfloat16, device=x.device)
+        out = _new((L, D), torch.bfloat16, x.device, stream)
     if ws is None:
-        ws = alloc_workspace(int(lib().vdn_hybrid_fuse_mxfp8_workspace(L, D, H)), x.device)
+        ws = alloc_workspace(int(lib().vdn_hybrid_fuse_mxfp8_workspace(L, D, H)), x.device,
+                             stream)
     _check(lib().vdn_hybrid_fuse_mxfp8(L, D, H, _ptr(x), _ptr(o_s), _ptr(o_vda), _ptr(wg[0]),
                                        _ptr(wg[1]), _ptr(gamma), float(eps), _ptr(wo[0]),
                                        _ptr(wo[1]), _ptr(out), _ptr(ws), ws.numel(),
@@ -524,9 +529,9 @@ def window_attn(q, k, v, T, N, H, d, chunk_frames=5, window_chunks=1, anchors=3,
     _need_cuda(q, k, v, out, lse, ws, ctx_k, ctx_v)
     shape = _shape(T, N, H, d)
     if out is None:
-        out = torch.empty((T * N, H * d), dtype=torch.bfloat16, device=q.device)
+        out = _new((T * N, H * d), torch.bfloat16, q.device, stream)
     if ws is None:
-        ws = alloc_workspace(window_attn_workspace(T, N, H, d), q.device)
+        ws = alloc_workspace(window_attn_workspace(T, N, H, d), q.device, stream)
     if ctx_k is None:
         code = lib().vdn_window_attn(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), q.stride(0),
                                      int(chunk_frames), int(window_chunks), int(anchors),
@@ -557,9 +562,9 @@ def window_attn_mxfp8(q, k, v, T, N, H, d, chunk_frames=5, window_chunks=1, anch
     _need_cuda(q, k, v, out, lse, ws)
     shape = _shape(T, N, H, d)
     if out is None:
-        out = torch.empty((T * N, H * d), dtype=torch.bfloat16, device=q.device)
+        out = _new((T * N, H * d), torch.bfloat16, q.device, stream)
     if ws is None:
-        ws = alloc_workspace(window_attn_mxfp8_workspace(T, N, H, d), q.device)
+        ws = alloc_workspace(window_attn_mxfp8_workspace(T, N, H, d), q.device, stream)
     code = lib().vdn_window_attn_mxfp8(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
                                        q.stride(0), int(chunk_frames), int(window_chunks),
                                        int(anchors), float(scale), _ptr(out), out.stride(0),
@@ -580,9 +585,9 @@ def hybrid_fuse(x, o_s, o_vda, W_gs, W_gl, gamma, W_os, W_ol, H, eps=1e-6, out=N
     _need_cuda(x, o_s, o_vda, W_gs, W_gl, gamma, W_os, W_ol, out, ws)
     L, D = x.shape
     if out is None:
-        out = torch.empty((L, D), dtype=torch.bfloat16, device=x.device)
+        out = _new((L, D), torch.bfloat16, x.device, stream)
     if ws is None:
-        ws = alloc_workspace(hybrid_fuse_workspace(L, D, H), x.device)
+        ws = alloc_workspace(hybrid_fuse_workspace(L, D, H), x.device, stream)
     code = lib().vdn_hybrid_fuse(int(L), int(D), int(H), _ptr(x), _ptr(o_s), _ptr(o_vda),
                                  _ptr(W_gs), _ptr(W_gl), _ptr(gamma), float(eps), _ptr(W_os),
                                  _ptr(W_ol), _ptr(out), _ptr(ws), ws.numel(), _stream(stream))
@@ -597,10 +602,10 @@ def hybrid_fuse_shard(x, o_s_local, o_vda_local, W_gs, W_gl, gamma, W_os, W_ol, 
     L, D = x.shape
     H_local = o_s_local.shape[1] // d
     if out is None:
-        out = torch.empty((L, D), dtype=torch.float32, device=x.device)
+        out = _new((L, D), torch.float32, x.device, stream)
     if ws is None:
         ws = alloc_workspace(int(lib().vdn_hybrid_fuse_shard_workspace(L, D, H_local, d)),
-                             x.device)
+                             x.device, stream)
     code = lib().vdn_hybrid_fuse_shard(int(L), int(D), int(H_local), int(d), int(head0),
                                        _ptr(x), _ptr(o_s_local), _ptr(o_vda_local),
                                        o_s_local.stride(0), _ptr(W_gs), _ptr(W_gl), _ptr(gamma),
@@ -621,7 +626,7 @@ def hybrid_fuse_shard_rs(x, o_s_local, o_vda_local, W_gs, W_gl, gamma, W_os, W_o
     H_local = o_s_local.shape[1] // d
     if ws is None:
         ws = alloc_workspace(int(lib().vdn_hybrid_fuse_shard_workspace(L, D, H_local, d)),
-                             x.device)
+                             x.device, stream)
     ptrs = (_P * len(owners))(*[t.data_ptr() for t in owners])
     code = lib().vdn_hybrid_fuse_shard_rs(int(L), int(D), int(H_local), int(d), int(head0),
                                           _ptr(x), _ptr(o_s_local), _ptr(o_vda_local),
@@ -1149,10 +1154,10 @@ class HybridLayer:
     def _to_device(self, tensors, stream):
         if all(t.is_cuda for t in tensors):
             return tensors
-        if self._staging is None:
-            self._staging = [torch.empty(t.shape, dtype=t.dtype, device=self.device)
-                             for t in tensors]
         with torch.cuda.stream(stream):
+            if self._staging is None:
+                self._staging = [torch.empty(t.shape, dtype=t.dtype, device=self.device)
+                                 for t in tensors]
             for dst, src in zip(self._staging, tensors):
                 dst.copy_(src, non_blocking=True)
         return self._staging
@@ -1259,16 +1264,18 @@ class HybridLayer:
         groups = self._head_groups()
         if getattr(self, "_stages", None) is None:
             b0 = batches[0]
-            self._stages = [[torch.empty(t.shape, dtype=t.dtype, device=dev) for t in b0]
+            with torch.cuda.stream(stream):  # its memory; the copies wait for it below
+                self._stages = [[torch.empty(t.shape, dtype=t.dtype, device=dev) for t in b0]
+                                for _ in range(2)]
+                self._ys = [torch.empty((self.L, self.D), dtype=torch.bfloat16, device=dev)
                             for _ in range(2)]
-            self._ys = [torch.empty((self.L, self.D), dtype=torch.bfloat16, device=dev)
-                        for _ in range(2)]
         if getattr(self, "_grp_key", None) != tuple(groups):
             # per head group: its beta and alpha columns, contiguous (rebuilt
             # whenever the grouping changes)
-            self._grp_ba = [(torch.empty((self.L, hg), dtype=torch.float32, device=dev),
-                             torch.empty((T, hg), dtype=torch.float32, device=dev))
-                            for _, hg in groups]
+            with torch.cuda.stream(stream):
+                self._grp_ba = [(torch.empty((self.L, hg), dtype=torch.float32, device=dev),
+                                 torch.empty((T, hg), dtype=torch.float32, device=dev))
+                                for _, hg in groups]
             self._grp_key = tuple(groups)
         if len(self._grp_ba) != len(groups):
             raise RuntimeError("forward_many: head-group buffers out of step with the grouping")
