@@ -512,9 +512,10 @@ VDN_API vdn_status vdn_qk_norm_rope_backward(
  * Products run in bf16 with fp32 accumulation, P rounded to bf16 for the
  * product with V; sums and maxima in fp32.  Queries are taken in tiles of up
  * to 256: a NaN or infinity in a key or value that one of a tile's queries
- * sees can reach the others of the tile, and only those; rows of other
- * sequences, or of none, never reach a sequence's results, not even their
- * rounding.
+ * sees can reach the others of the tile, and only those; what stands in rows
+ * of other sequences, or of none, never reaches a sequence's results, not
+ * even their rounding (their number can reach the rounding: keys are split
+ * by the shape alone).
  * Calls that may run at the same time (other streams, graphs replayed side by
  * side) need a workspace each, here and in the calls below.
  * ------------------------------------------------------------------------ */
@@ -568,7 +569,8 @@ VDN_API vdn_status vdn_sink_attn_backward(const vdn_sink_shape* shape, const voi
  *
  * q, o     : [B, ld] bf16, H heads;  k_new, v_new: [B, ld_new] bf16, H_kv heads
  * k_cache, v_cache: bf16, slot s of sequence b at b * batch_stride +
- *            s * ld_cache elements (no two sequences may share a cache)
+ *            s * ld_cache elements, one cache behind another: with B > 1
+ *            batch_stride is at least (slots - 1) * ld_cache + H_kv * d
  * positions: device int32 [B]; a negative one marks an inactive sequence:
  *            its cache and its row of o stay as they are
  * scale    : <= 0 selects 1/sqrt(d)

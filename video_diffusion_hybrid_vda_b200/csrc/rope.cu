@@ -24,7 +24,8 @@
 // memory and L1: 42336 rows of 24 + 24 heads of 128 took 234 us).  What keeps
 // the memory busy is bytes in flight: loads go through a cp.async ring in
 // shared memory in which every thread has its own slots (no barrier), so they
-// cost no registers (prefetched into registers: 208 us; now 179 us, 5.8 TB/s).
+// cost no registers (prefetched into registers: 208 us, then 179 us; 175 to
+// 194 us by the box, 5.4 to 5.9 TB/s).
 // Blocks that walk row groups in turn instead of one group a block: 207 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -29,13 +29,14 @@
 //
 // Bound: the chain score product -> softmax -> product with V of a row tile,
 // which the other row tile half hides (two S and two O accumulators fill TMEM
-// at d = 128).  16384 tokens, 16 heads over 4, window 4096: 430 to 460 us, 1.05
-// to 1.12 PFLOP/s of visible pairs (0.64 to 0.69 of the burst rate of a large
-// product, 0.76 to 0.82 of its sustained one); tensor and exponential pipes
-// each 40 % busy.  Also measured there: a quarter of the exponentials on the
-// FMA pipe 500 us, two warpgroups a row tile 513, key tiles of up to 64 valid
-// keys taken by halves 456 in place of 450 (and 15.4 in place of 16.2 us for
-// three short sequences).
+// at d = 128).  16384 tokens, 16 heads over 4, window 4096: 432 to 514 us by the
+// box and its clocks under the power cap (eager and in a graph alike: 488 to 502
+// and 498 us on one box), 0.94 to 1.11 PFLOP/s of visible pairs (0.57 to 0.68 of
+// the burst rate of a large product, 0.68 to 0.81 of its sustained one); tensor
+// and exponential pipes each 40 % busy.  Also measured, on a box where it took
+// 450 us: a quarter of the exponentials on the FMA pipe 500, two warpgroups a row
+// tile 513, key tiles of up to 64 valid keys taken by halves 456 (and 15.4 in
+// place of 16.2 us for three short sequences).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -575,7 +576,9 @@ __global__ void __launch_bounds__(256) sink_combine_kernel(const SinkDims dims, 
 // without a split, 64 over 6000 keys 19.6 and 22.3 with four tiles a split, 64
 // over 24000 keys 30 with 32 splits and 35.7 with 18; 1500 tokens of 6 heads over
 // 2 18.7 and 23.2 without; but 600 tokens of 8 heads 17.7 in five splits and 14.4
-// in one.
+// in one.  The walk is bounded by the window and by the keys of all sequences
+// together: many short sequences under a window that forgets nothing are split
+// although each has a tile or two (16 of 100 tokens, 2 heads: five splits).
 SinkCut sink_cut(const vdn_sink_shape& s) {
   SinkCut c{256, 1};
   const int group = s.H / s.H_kv, mean = (s.Lq + s.B - 1) / s.B;
