@@ -166,3 +166,21 @@ def test_captured_on_a_stream_that_is_given(vdn):
         graph.replay()
         torch.cuda.synchronize()
         assert _same(got, ref)
+
+
+def test_captured_on_a_forked_stream(vdn):
+    """Two calls side by side in one graph, each with memory of its own."""
+    calls = [_sink(40, 3000)(vdn), _sink(700, 700)(vdn)]
+    refs, st, graph = [c() for c in calls], torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        st.wait_stream(here)
+        got = [calls[0](stream=st), calls[1]()]
+        here.wait_stream(st)
+    for _ in range(2):
+        for g in got:
+            g[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(_same(g, r) for g, r in zip(got, refs))
