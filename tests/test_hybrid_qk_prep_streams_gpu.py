@@ -10,6 +10,7 @@ from video_diffusion_hybrid_vda_b200 import synth
 
 pytestmark = pytest.mark.gpu
 
+S_T = 6              # frames
 DELAY = 100_000_000  # cycles, some 50 ms: what a stream does behind it comes last
 
 
@@ -21,7 +22,7 @@ def vdn():
 
 
 def _case(vdn, d=64, **kw):
-    s = synth.Shape(6, 96, 4, d)
+    s = synth.Shape(S_T, 96, 4, d)
     x = synth.make_inputs(s, seed=5, device="cuda", with_fuse=True)
     x["k"] = x["k"] * 5
     layer = vdn.HybridLayer(s.T, s.N, s.H, s.d, x["W_gs"], x["W_gl"], x["W_os"], x["W_ol"],
@@ -103,6 +104,16 @@ def test_values_of_another_type_or_size_are_refused(vdn, bad):
     s, x, layer, ref = _case(vdn)
     with pytest.raises(ValueError):
         layer.forward(x["q"], x["k"], bad(x["v"]), x["beta"], x["alpha"], x["x"])
+
+
+@pytest.mark.parametrize("other", [
+    lambda v: torch.cat([v, v[:5]]), lambda v: v.view(S_T, -1, v.shape[1]),
+    lambda v: v.view(len(v), 4, -1),
+    lambda v: torch.stack([v, v, v], 1)[:, 1].unflatten(1, (4, -1))])
+def test_values_of_another_shape_or_with_more_rows(vdn, other):
+    s, x, layer, ref = _case(vdn)
+    y = layer.forward(x["q"], x["k"], other(x["v"]), x["beta"], x["alpha"], x["x"])
+    assert torch.equal(y, ref) and layer.status() == 0
 
 
 def test_captured_with_a_fused_projection_beside_contiguous_calls(vdn):

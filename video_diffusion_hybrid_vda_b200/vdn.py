@@ -1171,10 +1171,10 @@ class HybridLayer:
         address no multiple of 16 bytes, its columns apart) is copied, on
         ``stream`` like all the rest."""
         L, D, bf16 = self.L, self.D, torch.bfloat16
-        if v.dtype is not bf16 or v.numel() != L * D:
+        if v.dtype is not bf16 or v.numel() < L * D or v.numel() % D:
             raise ValueError(f"v: {v.dtype} {tuple(v.shape)}, expected {bf16} [{L}, {D}]")
         with torch.cuda.stream(stream):
-            v = v.reshape(L, D)
+            v = v.reshape(-1, D)[:L]
             ld = v.stride(0)
             if v.stride(1) != 1 or ld < D or ld % 8 or v.data_ptr() % 16:
                 v, ld = torch.empty((L, D), dtype=bf16, device=v.device).copy_(v), D
